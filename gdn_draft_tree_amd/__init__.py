@@ -16,7 +16,19 @@ target, as hand-written gfx950 (MI355X) HIP kernels behind a C ABI (include/gdnt
     acc  = gdntree_accept_build(tree, target_argmax, P, *next_lattice, N, next_tree)
     o    = gdntree_accept_commit_verify(tree, target_argmax, k, v, alpha, beta, P, next_tree, *next_rows, state)
 
-Importing this package loads libgdntree.so and raises if it has not been built.
+The target's attention layers over the same tree, and acceptance at a temperature
+(include/gdntree_target.h):
+
+    cache = KVCache.empty(layers, pages, H_kv, page_size, d, torch.float8_e4m3fn)
+    gdntree_cache_write(cache, layer, table, ctx_len, k, v, count=tree.n_nodes)   # per attention layer
+    o    = gdntree_attend(q, cache, layer, table, ctx_len, tree=tree)
+    acc  = gdntree_accept_sample(tree, logits, temperature, uniform, P)
+    gdntree_commit(tree, acc[0], acc[2], k, v, alpha, beta, state, P)             # the GDN layers' states
+    gdntree_cache_commit(cache, table, ctx_len, acc[0], acc[2], N)                # every attention layer
+    kv   = gdntree_cache_read(cache, layer, table, start, R)
+
+Importing this package loads libgdntree.so and libgdntree_target.so and raises if they have not
+been built.
 """
 from ._binding import (EXPORTED, GDNTREE_BF16, GDNTREE_ERR_ARG, GDNTREE_ERR_DEVICE,  # noqa: F401
                        GDNTREE_ERR_UNSUPPORTED, GDNTREE_F32, GDNTREE_OK, LIB, LIB_PATH, CTree,
@@ -25,3 +37,6 @@ from ._binding import (EXPORTED, GDNTREE_BF16, GDNTREE_ERR_ARG, GDNTREE_ERR_DEVI
                        gdntree_accept_commit_verify, gdntree_build,
                        gdntree_build_cond, gdntree_build_shared, gdntree_commit, gdntree_commit_build,
                        gdntree_markov_edges, gdntree_status_str, gdntree_verify)
+from ._target import (GDNTREE_CACHE_BF16, GDNTREE_CACHE_E4M3, TARGET_EXPORTED, TARGET_LIB,  # noqa: F401
+                      TARGET_LIB_PATH, CCache, KVCache, gdntree_accept_sample, gdntree_attend,
+                      gdntree_cache_commit, gdntree_cache_read, gdntree_cache_write)

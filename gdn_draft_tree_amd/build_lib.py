@@ -1,4 +1,4 @@
-"""Builds libgdntree.so (the gfx950 kernels and the C ABI) with hipcc.
+"""Builds libgdntree.so and libgdntree_target.so (the gfx950 kernels and their C ABIs) with hipcc.
 
     python __graft_entry__.py      (or __graft_entry__.build())
 """
@@ -13,6 +13,9 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libgdntree.so")
 SOURCES = ["gdntree_api.hip", "build_tree.hip", "verify_tree.hip", "accept_commit.hip", "commit_build.hip",
            "shared_budget.hip", "markov_edges.hip"]
+# the target's attention layers and sampled acceptance, a library with a header of its own
+TARGET_SOURCES = ["target_api.hip", "kv_cache.hip", "attend.hip", "accept_sample.hip"]
+TARGET_LIB = os.path.join(HERE, "libgdntree_target.so")
 # the benchmark's streaming probe, in a library of its own (not part of the path's ABI)
 PROBE_SOURCES = ["stream_probe.hip"]
 PROBE_LIB = os.path.join(HERE, "libgdntree_probe.so")
@@ -26,6 +29,7 @@ FLAGS = [
 
 def build(verbose: bool = False, extra: list[str] | None = None) -> str:
     _build_one(PROBE_LIB, PROBE_SOURCES, verbose, extra)
+    _build_one(TARGET_LIB, TARGET_SOURCES, verbose, extra)
     return _build_one(LIB, SOURCES, verbose, extra)
 
 

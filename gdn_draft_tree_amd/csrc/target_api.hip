@@ -1,0 +1,176 @@
+// C-ABI entry points of libgdntree_target.so: host-side argument validation, then the kernel
+// launches.  No allocation, no synchronisation, no exceptions across the boundary.
+
+#include <math.h>
+
+#include "target_internal.h"
+
+#define GDNTREE_EXPORT extern "C" __attribute__((visibility("default")))
+
+namespace {
+
+using namespace gdntree;
+
+bool dtype_ok(int d) { return d == GDNTREE_F32 || d == GDNTREE_BF16; }
+bool aligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+gdntree_status device_ok() {
+  int dev = -1;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0) {
+    (void)hipGetLastError();
+    return GDNTREE_ERR_DEVICE;
+  }
+  return GDNTREE_OK;
+}
+
+gdntree_status check_cache(const gdntree_cache &c, const int32_t *table, int max_pages) {
+  if (!c.k || !c.v || !table) return GDNTREE_ERR_ARG;
+  if (c.dtype != GDNTREE_CACHE_BF16 && c.dtype != GDNTREE_CACHE_E4M3) return GDNTREE_ERR_ARG;
+  if (c.dtype == GDNTREE_CACHE_E4M3 && (!c.k_scale || !c.v_scale || !aligned(c.k_scale) || !aligned(c.v_scale)))
+    return GDNTREE_ERR_ARG;
+  if (!aligned(c.k) || !aligned(c.v)) return GDNTREE_ERR_ARG;
+  if (c.L <= 0 || c.pages <= 0 || c.H_kv <= 0 || c.page_size <= 0 || c.d <= 0 || max_pages <= 0) return GDNTREE_ERR_ARG;
+  if ((c.d != 64 && c.d != 128) || c.page_size < kMinPage || c.page_size > kMaxPage || (c.page_size & (c.page_size - 1)))
+    return GDNTREE_ERR_UNSUPPORTED;
+  return GDNTREE_OK;
+}
+
+// One layer of a checked cache (layer 0 for calls over all of them).
+CacheView view(const gdntree_cache &c, int layer, const int32_t *table, int max_pages) {
+  CacheView v;
+  const long long rows = (long long)c.pages * c.H_kv * c.page_size;
+  const size_t row_bytes = (size_t)c.d * (c.dtype == GDNTREE_CACHE_E4M3 ? 1 : 2);
+  v.k = static_cast<unsigned char *>(c.k) + (size_t)layer * rows * row_bytes;
+  v.v = static_cast<unsigned char *>(c.v) + (size_t)layer * rows * row_bytes;
+  v.ks = c.dtype == GDNTREE_CACHE_E4M3 ? c.k_scale + (size_t)layer * rows : nullptr;
+  v.vs = c.dtype == GDNTREE_CACHE_E4M3 ? c.v_scale + (size_t)layer * rows : nullptr;
+  v.table = table;
+  v.pages = c.pages;
+  v.H = c.H_kv;
+  v.shift = __builtin_ctz((unsigned)c.page_size);
+  v.max_pages = max_pages;
+  v.layer_rows = rows;
+  return v;
+}
+
+gdntree_status rows_call(const gdntree_cache &cache, int layer, const int32_t *table, int max_pages,
+                         const int32_t *start, const int32_t *count, int B, int R, gdntree_dtype dtype, void *k,
+                         void *v, bool write, hipStream_t stream) {
+  if (gdntree_status st = check_cache(cache, table, max_pages); st != GDNTREE_OK) return st;
+  if (!start || !k || !v || !aligned(k) || !aligned(v)) return GDNTREE_ERR_ARG;
+  if (layer < 0 || layer >= cache.L || B <= 0 || R <= 0 || !dtype_ok(dtype)) return GDNTREE_ERR_ARG;
+  // 256 lanes hold 256 * 8 / d rows
+  const __int128 threads = (__int128)B * R * cache.H_kv * (cache.d / 8);
+  if (threads / 256 >= 0x7ffffffeLL) return GDNTREE_ERR_UNSUPPORTED;
+  if (gdntree_status st = device_ok(); st != GDNTREE_OK) return st;
+  RowsParams p;
+  p.c = view(cache, layer, table, max_pages);
+  p.start = start; p.count = count;
+  p.k = k; p.v = v;
+  p.B = B; p.R = R; p.D = cache.d;
+  p.fp8 = cache.dtype == GDNTREE_CACHE_E4M3;
+  p.rows_bf16 = dtype == GDNTREE_BF16;
+  if ((write ? launch_cache_write(p, stream) : launch_cache_read(p, stream)) != hipSuccess) return GDNTREE_ERR_DEVICE;
+  return GDNTREE_OK;
+}
+
+bool attend_sizes(int B, int R, int H_q, int H_kv, int d) { return B > 0 && R > 0 && H_q > 0 && H_kv > 0 && d > 0; }
+bool attend_limits(int R, int H_q, int H_kv, int d) {
+  return R <= kMaxSlots && H_q % H_kv == 0 && H_q / H_kv <= kMaxGroup && (d == 64 || d == 128);
+}
+
+}  // namespace
+
+GDNTREE_EXPORT gdntree_status gdntree_cache_write(gdntree_cache cache, int layer, const int32_t *table, int max_pages,
+                                                  const int32_t *start, const int32_t *count, int B, int R,
+                                                  gdntree_dtype in_dtype, const void *k, const void *v,
+                                                  hipStream_t stream) {
+  return rows_call(cache, layer, table, max_pages, start, count, B, R, in_dtype, const_cast<void *>(k),
+                   const_cast<void *>(v), true, stream);
+}
+
+GDNTREE_EXPORT gdntree_status gdntree_cache_read(gdntree_cache cache, int layer, const int32_t *table, int max_pages,
+                                                 const int32_t *start, const int32_t *count, int B, int R,
+                                                 gdntree_dtype out_dtype, void *k, void *v, hipStream_t stream) {
+  return rows_call(cache, layer, table, max_pages, start, count, B, R, out_dtype, k, v, false, stream);
+}
+
+GDNTREE_EXPORT gdntree_status gdntree_cache_commit(gdntree_cache cache, const int32_t *table, int max_pages,
+                                                   const int32_t *ctx_len, int B, int N, int P, const int32_t *acc_len,
+                                                   const int32_t *acc_node, hipStream_t stream) {
+  if (gdntree_status st = check_cache(cache, table, max_pages); st != GDNTREE_OK) return st;
+  if (!ctx_len || !acc_len || !acc_node) return GDNTREE_ERR_ARG;
+  if (B <= 0 || N <= 0 || P <= 0) return GDNTREE_ERR_ARG;
+  if (N > kMaxN || P > kMaxP) return GDNTREE_ERR_UNSUPPORTED;
+  const __int128 blocks = (__int128)cache.L * B * cache.H_kv;
+  if (blocks >= 0x7fffffffLL) return GDNTREE_ERR_UNSUPPORTED;
+  if (gdntree_status st = device_ok(); st != GDNTREE_OK) return st;
+  CacheCommitParams p;
+  p.c = view(cache, 0, table, max_pages);
+  p.ctx = ctx_len; p.acc_len = acc_len; p.acc_node = acc_node;
+  p.B = B; p.N = N; p.P = P; p.L = cache.L; p.D = cache.d;
+  p.fp8 = cache.dtype == GDNTREE_CACHE_E4M3;
+  if (launch_cache_commit(p, stream) != hipSuccess) return GDNTREE_ERR_DEVICE;
+  return GDNTREE_OK;
+}
+
+GDNTREE_EXPORT size_t gdntree_attend_workspace(int B, int R, int H_q, int H_kv, int d) {
+  if (!attend_sizes(B, R, H_q, H_kv, d) || !attend_limits(R, H_q, H_kv, d)) return 0;
+  return attend_workspace(B, R, H_q / H_kv, H_kv, d);
+}
+
+GDNTREE_EXPORT gdntree_status gdntree_attend(gdntree_cache cache, int layer, const int32_t *table, int max_pages,
+                                             const int32_t *ctx_len, const uint64_t *anc, const int32_t *n_rows, int B,
+                                             int R, int H_q, gdntree_dtype dtype, const void *q, float scale, void *o,
+                                             void *workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (gdntree_status st = check_cache(cache, table, max_pages); st != GDNTREE_OK) return st;
+  if (!ctx_len || !q || !o || !workspace || !aligned(q) || !aligned(o) || !aligned(workspace)) return GDNTREE_ERR_ARG;
+  if (layer < 0 || layer >= cache.L || !attend_sizes(B, R, H_q, cache.H_kv, cache.d) || !dtype_ok(dtype))
+    return GDNTREE_ERR_ARG;
+  if (!(scale > 0.f) || !(scale < INFINITY)) return GDNTREE_ERR_ARG;
+  if (!attend_limits(R, H_q, cache.H_kv, cache.d) || !attend_fits(B, R, H_q / cache.H_kv, cache.H_kv))
+    return GDNTREE_ERR_UNSUPPORTED;
+  if (workspace_bytes < gdntree_attend_workspace(B, R, H_q, cache.H_kv, cache.d)) return GDNTREE_ERR_ARG;
+  if (gdntree_status st = device_ok(); st != GDNTREE_OK) return st;
+  AttendParams p;
+  p.c = view(cache, layer, table, max_pages);
+  p.ctx = ctx_len; p.n_rows = n_rows;
+  p.anc = reinterpret_cast<const unsigned long long *>(anc);
+  p.q = q; p.o = o;
+  p.part = static_cast<float *>(workspace);
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.B = B; p.R = R; p.G = H_q / cache.H_kv; p.D = cache.d;
+  p.fp8 = cache.dtype == GDNTREE_CACHE_E4M3;
+  p.rows_bf16 = dtype == GDNTREE_BF16;
+  if (launch_attend(p, stream) != hipSuccess) return GDNTREE_ERR_DEVICE;
+  return GDNTREE_OK;
+}
+
+GDNTREE_EXPORT size_t gdntree_accept_sample_workspace(int B, int N, int V) {
+  if (B <= 0 || N <= 0 || V <= 0 || N > kMaxN || V > kMaxVocab) return 0;
+  return accept_sample_workspace(B, N + 1, V);
+}
+
+GDNTREE_EXPORT gdntree_status gdntree_accept_sample(gdntree_tree tree, int B, int N, int P, int V, gdntree_dtype dtype,
+                                                    const void *logits, const float *temperature,
+                                                    const double *uniform, int32_t *acc_len, int32_t *acc_tok,
+                                                    int32_t *acc_node, void *workspace, size_t workspace_bytes,
+                                                    hipStream_t stream) {
+  if (!tree.parent || !tree.token || !tree.n_nodes || !logits || !temperature || !uniform || !acc_len || !acc_tok ||
+      !acc_node || !workspace || !aligned(workspace))
+    return GDNTREE_ERR_ARG;
+  if (B <= 0 || N <= 0 || P <= 0 || V <= 0 || !dtype_ok(dtype)) return GDNTREE_ERR_ARG;
+  if (reinterpret_cast<uintptr_t>(logits) & (dtype == GDNTREE_BF16 ? 1 : 3)) return GDNTREE_ERR_ARG;
+  if (N > kMaxN || P > kMaxP || V > kMaxVocab || !sample_fits(B, N + 1, V)) return GDNTREE_ERR_UNSUPPORTED;
+  if (workspace_bytes < accept_sample_workspace(B, N + 1, V)) return GDNTREE_ERR_ARG;
+  if (gdntree_status st = device_ok(); st != GDNTREE_OK) return st;
+  SampleParams p;
+  p.parent = tree.parent; p.token = tree.token; p.n_nodes = tree.n_nodes;
+  p.logits = logits; p.temperature = temperature; p.uniform = uniform;
+  p.acc_len = acc_len; p.acc_tok = acc_tok; p.acc_node = acc_node;
+  p.ws = workspace;
+  p.B = B; p.R = N + 1; p.P = P; p.V = V;
+  p.bf16 = dtype == GDNTREE_BF16;
+  if (launch_accept_sample(p, stream) != hipSuccess) return GDNTREE_ERR_DEVICE;
+  return GDNTREE_OK;
+}

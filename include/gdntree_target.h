@@ -1,0 +1,174 @@
+/*
+ * gdntree_target.h - C ABI of the gfx950 library for what surrounds the draft tree in the
+ * hybrid target's attention layers, and for acceptance at a temperature (libgdntree_target.so).
+ *
+ * gdntree.h verifies the tree in the Gated-DeltaNet layers, whose memory is a fixed-size state.
+ * The target's other layers attend to every earlier token, so they keep a key-value cache.  One
+ * decode step, per attention layer:
+ *   gdntree_cache_write    the tree rows' keys and values go into the cache, at the positions
+ *                          behind the committed tokens (optionally quantised to 8 bits)
+ *   gdntree_attend         every tree row attends to the committed positions and to its own
+ *                          ancestors (the tree mask, gdntree_tree.anc); a single new token is
+ *                          the tree of one row
+ * and once per step, for all layers:
+ *   gdntree_accept_sample  acceptance of drafted tokens against the target's distribution from
+ *                          given random numbers (gdntree_accept is its greedy form); its output
+ *                          is what gdntree_commit and gdntree_cache_commit take
+ *   gdntree_cache_commit   the accepted rows move together behind the committed tokens
+ * gdntree_cache_read reads positions back from the cache as rows.
+ *
+ * Conventions: those of gdntree.h (device pointers the caller owns, dense row-major layouts, no
+ * allocation, no synchronisation, host-side checks, nothing enqueued on an error, no global
+ * state).  Calls that need scratch memory take it from the caller: its size comes from the
+ * call's *_workspace function, and one workspace serves one call at a time (calls on one
+ * stream may share it; calls, or captured graphs, that can overlap need one each).  Its
+ * contents need not be set and mean nothing after the call.
+ */
+#ifndef GDNTREE_TARGET_H
+#define GDNTREE_TARGET_H
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "gdntree.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef enum { GDNTREE_CACHE_BF16 = 0, GDNTREE_CACHE_E4M3 = 1 } gdntree_cache_dtype;
+
+/*
+ * A paged key-value cache of L attention layers.  Position p of request b lives in page
+ * table[b][p / page_size], slot p % page_size, of every layer; `table` (i32 [B][max_pages]) and
+ * the lengths are arguments of the calls.
+ *
+ * E4M3: 8-bit codes (4 exponent, 3 mantissa bits, largest 448, no infinity, NaN 0x7f) with one
+ * power-of-two scale per (layer, token, head), held as its biased exponent byte (scale
+ * 2^(byte - 127)).  A code times its scale is a bf16 number, so what is read back, by
+ * gdntree_cache_read or by gdntree_attend, is exactly what was stored.
+ *
+ * Limits: page_size a power of two in [16, 256], d in {64, 128}; every pointer 16-byte aligned.
+ * Requests may share pages that are only read (a common prefix); a page that is written by a
+ * call must appear once in that call's table.
+ */
+typedef struct {
+  void *k, *v;                 /* [L][pages][H_kv][page_size][d]                             */
+  uint8_t *k_scale, *v_scale;  /* [L][pages][H_kv][page_size], E4M3 only (else ignored)      */
+  int L, pages, H_kv, page_size, d;
+  gdntree_cache_dtype dtype;
+} gdntree_cache;
+
+/*
+ * gdntree_cache_write - rows of one layer into the cache: row t < count[b] of request b goes to
+ * position start[b] + t (a prompt's rows, a step's tree rows, or one new token).
+ *
+ *   table  i32 [B][max_pages]        page ids in [0, pages)
+ *   start  i32 [B], count i32 [B]    count NULL: R rows each; else clipped to [0, R]
+ *   k, v   in_dtype [B][R][H_kv][d]
+ * BF16 cache: rounded to nearest even.  E4M3 cache: with amax the largest finite |x| of the row
+ * (one token, one head), the scale is the least 2^e, e >= -117, with amax <= 448 2^e, and each
+ * code is x 2^-e (exact) rounded to nearest even; infinities and NaN are stored as NaN.
+ * A row whose position lies outside [0, max_pages * page_size), or whose page id lies outside
+ * [0, pages), is not written.  Nothing else in the cache is touched.
+ */
+gdntree_status gdntree_cache_write(gdntree_cache cache, int layer, const int32_t *table, int max_pages,
+                                   const int32_t *start, const int32_t *count, int B, int R,
+                                   gdntree_dtype in_dtype, const void *k, const void *v, hipStream_t stream);
+
+/*
+ * gdntree_cache_read - the inverse: row t < count[b] of request b is position start[b] + t of
+ * one layer, in out_dtype (exactly: every cache value is a bf16 number).  Rows at or past
+ * count[b] are left as they were; a row whose position or page id is out of range (as above)
+ * reads as NaN.
+ */
+gdntree_status gdntree_cache_read(gdntree_cache cache, int layer, const int32_t *table, int max_pages,
+                                  const int32_t *start, const int32_t *count, int B, int R,
+                                  gdntree_dtype out_dtype, void *k, void *v, hipStream_t stream);
+
+/*
+ * gdntree_cache_commit - the accepted path's rows move together: for every layer and head,
+ * position ctx_len[b] + acc_node[b][i] is copied to ctx_len[b] + i for i < acc_len[b], as if all
+ * were read before any is written (codes and scales are copied, never requantised).  Afterwards
+ * the request holds ctx_len[b] + acc_len[b] committed positions; the slots behind them hold
+ * what is left of the tree and are overwritten by the next step.
+ *
+ *   ctx_len  i32 [B]        committed positions before the step
+ *   acc_len  i32 [B], acc_node i32 [B][P+1]   from gdntree_accept or gdntree_accept_sample
+ * A request whose path is malformed (acc_len outside [1, P+1], a first slot other than 0, slots
+ * not strictly increasing or past N), whose positions are out of range, or with a page id out of
+ * range on its path is left unchanged.  Limits: N <= 64, P <= 16.
+ */
+gdntree_status gdntree_cache_commit(gdntree_cache cache, const int32_t *table, int max_pages,
+                                    const int32_t *ctx_len, int B, int N, int P, const int32_t *acc_len,
+                                    const int32_t *acc_node, hipStream_t stream);
+
+/*
+ * gdntree_attend - attention of each request's new rows over its cache, one layer.
+ *
+ * Row t < n_rows[b] of request b (its keys and values already written at position
+ * ctx_len[b] + t) attends to the positions
+ *     p < ctx_len[b],   p = ctx_len[b] (slot 0),   and p = ctx_len[b] + s for its slots s < n_rows[b]:
+ * with `anc` the slots whose bit s-1 is set in anc[b][t] (a draft tree's ancestors-or-self, as
+ * gdntree_build writes them), without it every slot s <= t (a chain: new tokens in order).
+ *     o[b][t][h] = sum_p softmax_p(scale * q[b][t][h] . k[p][h / (H_q/H_kv)]) v[p][h / (H_q/H_kv)]
+ * What a row does not attend to (other branches, slots past n_rows, the rest of a page) has no
+ * effect on it, whatever it holds, NaN and infinities included.
+ *
+ *   q, o     dtype [B][R][H_q][d]; rows t >= n_rows[b] are neither read nor written
+ *   anc      u64 [B][R] or NULL
+ *   n_rows   i32 [B] or NULL (R rows each); a request with n_rows outside [1, R] gets no output
+ *   scale    > 0, finite (d^-1/2 usually)
+ *   workspace  at least gdntree_attend_workspace(...) bytes, 16-byte aligned
+ * bf16 rows: exact products, fp32 sums and softmax statistics; the softmax weights enter the
+ * product with the values rounded to bf16, and o is rounded once.  fp32 rows: q and the weights
+ * are split into three bf16 parts, so that every product is exact and the sums are fp32.
+ * A request whose ctx_len is negative, whose positions exceed max_pages * page_size, or which
+ * meets a page id outside [0, pages) gets NaN in its rows < n_rows[b].
+ * Limits: R <= 65, H_q a multiple of H_kv, H_q / H_kv <= 16.
+ */
+size_t gdntree_attend_workspace(int B, int R, int H_q, int H_kv, int d);
+gdntree_status gdntree_attend(gdntree_cache cache, int layer, const int32_t *table, int max_pages,
+                              const int32_t *ctx_len, const uint64_t *anc, const int32_t *n_rows, int B, int R,
+                              int H_q, gdntree_dtype dtype, const void *q, float scale, void *o,
+                              void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * gdntree_accept_sample - acceptance of a draft tree against the target's distributions
+ * p_u = softmax(logits[b][u] / temperature[b]) from given random numbers, and the bonus token.
+ *
+ * Walk from the root u = 0: with c_1, c_2, ... the children of u in slot order and
+ * U = uniform[b][u], step to child c_i if
+ *     p_u(token c_1) + ... + p_u(token c_{i-1}) <= U < p_u(token c_1) + ... + p_u(token c_i)
+ * (a child repeating an earlier sibling's token has no mass of its own); else stop, and the
+ * bonus is the token x, not a child's, at which the running sum of p_u over the vocabulary
+ * without the children's tokens first exceeds U - sum_i p_u(token c_i).  The drafts are fixed
+ * given the lattice, so this is inverse-transform sampling from p_u with the vocabulary
+ * reordered: every emitted token has exactly the target's distribution, and a drafted child is
+ * accepted with the largest probability any lossless rule allows.  At most P drafts are accepted
+ * (tau <= P + 1).  temperature[b] = 0 takes the argmax (the lowest token id on a tie): the
+ * acceptance of gdntree_accept.
+ *
+ *   logits       dtype [B][N+1][V]; rows t < n_nodes[b] are read; -inf masks a token
+ *   temperature  f32 [B], >= 0
+ *   uniform      f64 [B][N+1], in [0, 1)
+ *   acc_len, acc_tok, acc_node   as gdntree_accept writes them
+ *   workspace    at least gdntree_accept_sample_workspace(...) bytes, 16-byte aligned
+ * Every weight is exp((l - max) / temperature).  The sums that place the bonus token are fp64;
+ * the normaliser that the accepted children are held to is a sum of fp32 exponentials (1e-7).
+ * A row that holds no distribution (NaN, +inf, or only -inf), or a temperature that is negative
+ * or not finite: the walk stops there and the bonus is -1.  A child's token outside [0, V) has no mass.
+ * A request with n_nodes outside [1, N+1] gets no output.  Reads tree.parent, tree.token and
+ * tree.n_nodes.  Limits: N <= 64, P <= 16, V <= 2^24.
+ */
+size_t gdntree_accept_sample_workspace(int B, int N, int V);
+gdntree_status gdntree_accept_sample(gdntree_tree tree, int B, int N, int P, int V, gdntree_dtype dtype,
+                                     const void *logits, const float *temperature, const double *uniform,
+                                     int32_t *acc_len, int32_t *acc_tok, int32_t *acc_node, void *workspace,
+                                     size_t workspace_bytes, hipStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* GDNTREE_TARGET_H */

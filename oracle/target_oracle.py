@@ -1,0 +1,107 @@
+"""fp64 CPU oracle of the target's attention layers and of sampled acceptance (test
+infrastructure only): plain numpy, from the definitions, sharing no code with the HIP path."""
+from __future__ import annotations
+
+import numpy as np
+
+E4M3_MAX = 448.0
+
+
+def e4m3_round(y):
+    """The e4m3 number nearest to y (|y| <= 448), ties to the even significand."""
+    y = np.asarray(y, np.float64)
+    _, e = np.frexp(y)
+    step = np.ldexp(1.0, np.maximum(e - 1, -6) - 3)
+    return np.round(y / step) * step            # numpy rounds halves to even
+
+
+def quantise_rows(x):
+    """(values of the codes, biased scale exponents) of rows x [..., d]: the scale is the least 2^e,
+    e >= -117, with the largest finite |x| at most 448 2^e; what is not finite becomes NaN."""
+    x = np.asarray(x, np.float64)
+    ok = np.isfinite(x)
+    amax = np.where(ok, np.abs(x), 0.0).max(-1)
+    e = np.full(amax.shape, -117)
+    for i in np.ndindex(amax.shape):
+        while amax[i] > E4M3_MAX * 2.0 ** float(e[i]):
+            e[i] += 1
+    with np.errstate(invalid="ignore"):
+        code = np.where(ok, e4m3_round(np.where(ok, x, 0.0) / np.exp2(e.astype(np.float64))[..., None]), np.nan)
+    return code, e + 127
+
+
+def visible(n, ctx, anc=None):
+    """[n][ctx + n]: which positions row t attends to (anc: its ancestor bitmasks; None: a chain)."""
+    see = np.zeros((n, ctx + n), bool)
+    see[:, :ctx] = True
+    for t in range(n):
+        for s in range(n):
+            see[t, ctx + s] = s <= t if anc is None else s == 0 or (int(anc[t]) >> (s - 1)) & 1 == 1
+    return see
+
+
+def attend(q, k, v, see, scale):
+    """One request: q [n][H_q][d], k, v [T][H_kv][d], see [n][T].  Returns o and, per output, the
+    weighted mean of |v| and the row's largest scale * sum |q k| (what rounding errors scale with)."""
+    n, Hq, d = q.shape
+    G = Hq // k.shape[1]
+    o, mean, big = np.zeros((n, Hq, d)), np.zeros((n, Hq, d)), np.zeros((n, Hq))
+    for h in range(Hq):
+        kk, vv = k[:, h // G], v[:, h // G]
+        for t in range(n):
+            idx = np.flatnonzero(see[t])
+            s = scale * (kk[idx] @ q[t, h])
+            with np.errstate(invalid="ignore"):
+                w = np.exp(s - s.max())
+                p = w / w.sum()
+                o[t, h], mean[t, h] = p @ vv[idx], p @ np.abs(vv[idx])
+            big[t, h] = (scale * (np.abs(kk[idx]) @ np.abs(q[t, h]))).max()
+    return o, mean, big
+
+
+def commit_path(rows, ctx, path):
+    """rows [T][...] of one request with the accepted slots moved together behind ctx."""
+    out = rows.copy()
+    for i, s in enumerate(path):
+        out[ctx + i] = rows[ctx + s]
+    return out
+
+
+def accept_sample(parent, token, n, logits, temperature, uniform, P):
+    """One request: the accepted slots, their tokens and the bonus.  logits [N+1][V], fp64."""
+    u, path, toks = 0, [0], []
+    bonus = -1
+    while 0.0 <= temperature < np.inf:
+        x = logits[u]
+        top = x.max() if not np.isnan(x).any() else np.nan
+        if not np.isfinite(top):
+            break
+        kids = [t for t in range(1, n) if parent[t] == u] if len(path) <= P else []
+        if temperature == 0.0:
+            bonus = int(np.flatnonzero(x == top)[0])
+            hit = [t for t in kids if token[t] == bonus]
+            nxt = hit[0] if hit else -1
+        else:
+            w = np.exp((x - top) / temperature)
+            at, run, nxt, gone = uniform[u] * w.sum(), 0.0, -1, []
+            for t in kids:
+                if 0 <= token[t] < len(w) and token[t] not in gone:
+                    gone.append(int(token[t]))
+                    if run <= at < run + w[token[t]]:
+                        nxt = t
+                        break
+                    run += w[token[t]]
+            if nxt < 0:
+                rest = w.copy()
+                rest[gone] = 0.0
+                c = np.cumsum(rest)
+                over = np.flatnonzero((c > max(0.0, at - run)) & (rest > 0))
+                some = np.flatnonzero(rest > 0)
+                bonus = int(over[0]) if len(over) else int(some[-1]) if len(some) else gone[-1]
+        if nxt < 0:
+            break
+        bonus = -1
+        u = nxt
+        path.append(u)
+        toks.append(int(token[u]))
+    return path, toks + [bonus]

@@ -1,0 +1,176 @@
+"""Acceptance at a temperature on the GPU against the oracle: accepted paths, tokens and the bonus,
+integer for integer, and the emitted tokens' distribution."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import target_oracle as T
+from tests.test_gpu_kv_cache import DT
+
+pytestmark = pytest.mark.gpu
+
+
+def random_trees(B, N, P, V, gen):
+    parent, token = np.full((B, N + 1), -1, np.int32), np.zeros((B, N + 1), np.int32)
+    for b in range(B):
+        de = [0]
+        for t in range(1, N + 1):
+            open_ = [s for s in range(t) if de[s] < P]
+            p = t - 1 if t <= min(P, 4) else open_[int(gen.integers(len(open_)))]
+            parent[b, t] = p
+            de.append(de[p] + 1)
+        token[b] = gen.integers(0, V, N + 1)
+    return parent, token
+
+
+def run(parent, token, n, logits, temp, uni, P, **kw):
+    import gdn_draft_tree_amd as g
+    B, R = parent.shape
+    tree = g.Tree.empty(B, R - 1, "cuda")
+    tree.parent.copy_(torch.from_numpy(parent))
+    tree.token.copy_(torch.from_numpy(token))
+    tree.n_nodes.copy_(torch.tensor(n, dtype=torch.int32))
+    acc = (torch.full((B,), 77, dtype=torch.int32, device="cuda"),) + tuple(
+        torch.full((B, P + 1), 77, dtype=torch.int32, device="cuda") for _ in range(2))
+    g.gdntree_accept_sample(tree, logits, torch.tensor(temp, dtype=torch.float32).cuda(), torch.from_numpy(uni).cuda(),
+                            P, acc=acc, **kw)
+    return [x.cpu().numpy() for x in acc]
+
+
+def check(got, parent, token, n, logits, temp, uni, P):
+    B, R = parent.shape
+    x = logits.double().cpu().numpy()
+    for b in range(B):
+        if not 1 <= n[b] <= R:
+            assert (got[0][b], *got[1][b], *got[2][b]) == (77,) * (2 * P + 3)
+            continue
+        path, toks = T.accept_sample(parent[b], token[b], n[b], x[b], float(np.float32(temp[b])), uni[b], P)
+        pad = [-1] * (P + 1 - len(path))
+        assert got[0][b] == len(path), b
+        assert got[2][b].tolist() == path + pad, b
+        assert got[1][b].tolist() == toks + pad, (b, got[1][b], toks)
+
+
+CASES = [  # B, N, P, V, dtype
+    (2, 1, 1, 1, "f32"), (3, 4, 4, 7, "bf16"), (4, 8, 4, 33, "f32"), (5, 24, 8, 1000, "bf16"), (3, 64, 16, 4097, "f32"),
+    (2, 64, 16, 8191, "bf16"), (3, 24, 8, 32000, "f32"), (2, 40, 12, 151936, "bf16"), (2, 24, 8, 151937, "bf16"),
+    (1, 16, 8, 300001, "f32"), (40, 64, 16, 260, "bf16"),
+]
+
+
+@pytest.mark.parametrize("B,N,P,V,kind", CASES)
+def test_matches_the_oracle(B, N, P, V, kind):
+    gen = np.random.default_rng(B * 1000 + N)
+    parent, token = random_trees(B, N, P, V, gen)
+    n = [N + 1 if b % 4 != 2 else 1 + b % (N + 1) for b in range(B)]
+    logits = torch.from_numpy(gen.normal(0, 2, (B, N + 1, V)).astype(np.float32))
+    for b in range(B):                       # drafts that are often taken
+        for t in range(1, N + 1):
+            logits[b, parent[b, t], token[b, t]] += np.log(V) + gen.uniform(0, 2)
+    logits = logits.to(DT[kind]).cuda()
+    temp = [0.0 if b % 5 == 3 else float(gen.uniform(0.3, 1.6)) for b in range(B)]
+    for _ in range(4):
+        uni = gen.random((B, N + 1))
+        check(run(parent, token, n, logits, temp, uni, P), parent, token, n, logits, temp, uni, P)
+
+
+def test_masked_faulty_and_tied_rows():
+    gen = np.random.default_rng(5)
+    B, N, P, V = 12, 6, 4, 9001
+    parent = np.tile(np.array([-1, 0, 0, 1, 1, 3, 0], np.int32), (B, 1))
+    token = np.tile(np.array([0, 5, 6, 7, 8, 9, 5], np.int32), (B, 1))       # slot 6 repeats slot 1's token
+    logits = torch.zeros(B, N + 1, V)
+    temp, n = [1.0] * B, [N + 1] * B
+    logits[0, :, :] = -np.inf                                                 # nothing left
+    logits[1, :, 20:] = -np.inf                                               # 20 tokens left
+    logits[2, 0, 8500] = np.nan
+    logits[3, 0, 8999] = np.inf
+    logits[4, 1, 0] = np.nan                                                  # only below slot 1
+    logits[4, 0, 5] = 60.0
+    logits[5, :, :] = -np.inf
+    logits[5, :, [5, 7, 9]] = 0.0                                             # children hold all the mass
+    temp[6] = 0.0                                                             # all tied: token 0
+    temp[7], logits[7, :, 5:7] = 0.0, 3.0                                     # two tied: the lower, a child
+    temp[8], logits[8, 0, 17] = 0.0, np.nan
+    temp[9], temp[10] = -1.0, np.inf
+    n[11] = 8                                                                 # out of range: no output
+    temp[1] = 1e-38                                                           # a temperature next to none
+    for dt in ("f32", "bf16"):
+        x = logits.to(DT[dt]).cuda()
+        for _ in range(6):
+            uni = gen.random((B, N + 1))
+            check(run(parent, token, n, x, temp, uni, P), parent, token, n, x, temp, uni, P)
+        for u in (0.0, 1.0 - 2.0 ** -53):
+            uni = np.full((B, N + 1), u)
+            check(run(parent, token, n, x, temp, uni, P), parent, token, n, x, temp, uni, P)
+
+
+def test_children_outside_the_vocabulary_and_p_limits():
+    gen = np.random.default_rng(6)
+    parent = np.array([[-1, 0, 0, 2, 3, 4]] * 2, np.int32)
+    token = np.array([[0, -3, 1, 2, 3, 40], [0, 1000, 1, 2, 3, 4]], np.int32)
+    logits = torch.zeros(2, 6, 5)
+    logits[0, :, 1:4], logits[1, :, 1:4] = 9.0, 9.0
+    x = logits.cuda()
+    for P in (1, 2, 3, 5):
+        for _ in range(5):
+            uni = gen.random((2, 6))
+            check(run(parent, token, [6, 6], x, [1.0, 1.0], uni, P), parent, token, [6, 6], x, [1.0, 1.0], uni, P)
+
+
+def test_greedy_equals_gdntree_accept():
+    import gdn_draft_tree_amd as g
+    gen = np.random.default_rng(8)
+    B, N, P, V = 16, 64, 16, 50
+    parent, token = random_trees(B, N, P, V, gen)
+    x = torch.from_numpy(gen.normal(0, 2, (B, N + 1, V)).astype(np.float32)).cuda()
+    got = run(parent, token, [N + 1] * B, x, [0.0] * B, gen.random((B, N + 1)), P)
+    tree = g.Tree.empty(B, N, "cuda")
+    tree.parent.copy_(torch.from_numpy(parent)), tree.token.copy_(torch.from_numpy(token)), tree.n_nodes.fill_(N + 1)
+    want = g.gdntree_accept(tree, x.argmax(-1).int().contiguous(), P)
+    for a, b in zip(got, want):
+        np.testing.assert_array_equal(a, b.cpu().numpy())
+
+
+def test_first_token_has_the_targets_distribution():
+    """512 requests of the same row and random numbers on a grid: counts per token within one grid cell
+    per interval border (each token is one interval of the reordered vocabulary)."""
+    B, V = 512, 23
+    gen = np.random.default_rng(9)
+    row = gen.normal(0, 1.5, V).astype(np.float32)
+    x = torch.from_numpy(np.tile(row, (B, 5, 1))).cuda()
+    parent = np.tile(np.array([-1, 0, 0, 1, 2], np.int32), (B, 1))
+    token = np.tile(np.array([0, 4, 11, 3, 2], np.int32), (B, 1))
+    uni = np.tile(((np.arange(B) + 0.5) / B)[:, None], (1, 5))
+    got = run(parent, token, [5] * B, x, [0.9] * B, uni, 4)
+    p = np.exp(row.astype(np.float64) / np.float64(np.float32(0.9)))
+    counts = np.bincount(got[1][:, 0], minlength=V)
+    assert (np.abs(counts - B * p / p.sum()) <= 1.0 + 1e-6).all()
+
+
+def test_captured_graph_and_other_stream():
+    import gdn_draft_tree_amd as g
+    gen = np.random.default_rng(11)
+    B, N, P, V = 3, 24, 8, 20011
+    parent, token = random_trees(B, N, P, V, gen)
+    tree = g.Tree.empty(B, N, "cuda")
+    tree.parent.copy_(torch.from_numpy(parent)), tree.token.copy_(torch.from_numpy(token)), tree.n_nodes.fill_(N + 1)
+    x = torch.from_numpy(gen.normal(0, 2, (B, N + 1, V)).astype(np.float32)).cuda()
+    rows = torch.arange(B).cuda()[:, None].expand(B, N)
+    x[rows, tree.parent[:, 1:].long(), tree.token[:, 1:].long()] += 11.0
+    temp, uni = torch.full((B,), 0.8, device="cuda"), torch.zeros(B, N + 1, dtype=torch.float64, device="cuda")
+    g.gdntree_accept_sample(tree, x, temp, uni, P)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        acc = g.gdntree_accept_sample(tree, x, temp, uni, P)
+    s = torch.cuda.Stream()
+    for _ in range(5):
+        uni.copy_(torch.from_numpy(gen.random((B, N + 1))))
+        want = g.gdntree_accept_sample(tree, x, temp, uni, P)
+        graph.replay()
+        s.wait_stream(torch.cuda.current_stream())
+        other = [g.gdntree_accept_sample(tree, x, temp, uni, P, stream=s) for _ in range(8)]
+        torch.cuda.synchronize()
+        for i in range(3):
+            assert torch.equal(acc[i], want[i]) and all(torch.equal(y[i], want[i]) for y in other)

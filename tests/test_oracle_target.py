@@ -1,0 +1,102 @@
+"""Pins of the attention-layer and sampled-acceptance oracle (CPU)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import target_oracle as T
+
+
+def test_e4m3_rounding_matches_the_format():
+    """Every e4m3 number rounds to itself, every midpoint to the even neighbour, and random numbers as
+    torch's conversion does."""
+    codes = torch.arange(0, 127, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy()  # 0 .. 448
+    np.testing.assert_array_equal(T.e4m3_round(codes), codes)
+    np.testing.assert_array_equal(T.e4m3_round(-codes), -codes)
+    mid = (codes[:-1] + codes[1:]) / 2
+    np.testing.assert_array_equal(T.e4m3_round(mid), np.where(np.arange(126) % 2 == 0, codes[:-1], codes[1:]))
+    x = np.random.default_rng(0).normal(0, 60, 20000).clip(-448, 448).astype(np.float32)
+    np.testing.assert_array_equal(T.e4m3_round(x), torch.from_numpy(x).to(torch.float8_e4m3fn).double().numpy())
+
+
+def test_quantise_hand_cases():
+    x = np.array([[448.0, 1.0], [449.0, 1.0], [0.0, 0.0], [896.0, -896.0], [np.inf, 7.0], [np.nan, 448.0 * 2.0 ** -20]])
+    code, byte = T.quantise_rows(x)
+    np.testing.assert_array_equal(byte, [127, 128, 10, 128, 121, 107])
+    np.testing.assert_array_equal(code[0], [448, 1])
+    np.testing.assert_array_equal(code[1], [224, 0.5])           # 224.5 lies between 224 and 240
+    np.testing.assert_array_equal(code[3], [448, -448])
+    assert np.isnan(code[4][0]) and code[4][1] == 448 and np.isnan(code[5][0]) and code[5][1] == 448
+
+
+def test_quantise_error_is_half_a_step():
+    x = np.random.default_rng(1).normal(0, 3, (200, 128))
+    code, byte = T.quantise_rows(x)
+    back = code * np.exp2(byte - 127.0)[:, None]
+    # normal codes: half a step, 2^-4 of the value; below 2^-6: half the smallest step
+    step = np.exp2(byte - 127.0)[:, None] * 2.0 ** -10
+    assert (np.abs(back - x) <= np.maximum(np.abs(x) * 2.0 ** -4, step)).all()
+    assert (np.abs(code).max(-1) > 208).all()                    # the range is used: amax / 2^e > 224, rounded
+
+
+def test_attend_equals_a_masked_softmax():
+    g = torch.Generator().manual_seed(2)
+    n, ctx, Hq, H, d = 5, 9, 4, 2, 8
+    q, k, v = (torch.randn(s, generator=g, dtype=torch.float64) for s in ((n, Hq, d), (ctx + n, H, d), (ctx + n, H, d)))
+    anc = [0, 1, 2, 1 | 4, 2 | 8]
+    for mask in (None, anc):
+        see = T.visible(n, ctx, mask)
+        o, _, _ = T.attend(q.numpy(), k.numpy(), v.numpy(), see, 0.3)
+        ref = torch.nn.functional.scaled_dot_product_attention(
+            q.permute(1, 0, 2), k.permute(1, 0, 2).repeat_interleave(2, 0), v.permute(1, 0, 2).repeat_interleave(2, 0),
+            attn_mask=torch.from_numpy(see), scale=0.3).permute(1, 0, 2)
+        np.testing.assert_allclose(o, ref.numpy(), rtol=1e-12, atol=1e-13)
+    assert T.visible(3, 0, [0, 1, 2])[2].tolist() == [True, False, True]
+    assert T.visible(3, 1, None)[1].tolist() == [True, True, True, False]
+
+
+def test_commit_path_moves_rows_as_if_read_first():
+    rows = np.arange(20)
+    np.testing.assert_array_equal(T.commit_path(rows, 3, [0, 2, 3, 9]), [0, 1, 2, 3, 5, 6, 12] + list(range(7, 20)))
+
+
+HAND = np.log(np.array([[0.1, 0.2, 0.3, 0.4]] * 4))
+
+
+@pytest.mark.parametrize("u,path,toks", [
+    (0.0, [0, 1], [2, 0]), (0.29, [0, 1], [2, 0]), (0.31, [0, 2], [0, 0]), (0.39, [0, 2], [0, 0]),
+    (0.41, [0], [1]), (0.59, [0], [1]), (0.61, [0], [3]), (0.999, [0], [3])])
+def test_accept_sample_hand_case(u, path, toks):
+    """Children 2 (p 0.3) and 0 (p 0.1) in slot order; the rest is token 1 (0.2), then token 3 (0.4)."""
+    got = T.accept_sample([-1, 0, 0, 0], [9, 2, 0, 2], 4, HAND, 1.0, np.array([u, 0.0, 0.0, 0.0]), 4)
+    assert got == (path, toks)
+
+
+def test_accept_sample_emits_the_target_distribution():
+    """The first emitted token has the target's distribution, whatever the tree offers (exactly: the
+    random numbers are a fine grid)."""
+    rng = np.random.default_rng(3)
+    logits = rng.normal(0, 1.5, (4, 7))
+    grid = (np.arange(20000) + 0.5) / 20000
+    for temp in (0.5, 1.0, 1.7):
+        p = np.exp(logits[0] / temp) / np.exp(logits[0] / temp).sum()
+        count = np.zeros(7)
+        for u in grid:
+            _, toks = T.accept_sample([-1, 0, 0, 0], [0, 5, 2, 6], 4, logits, temp, np.full(4, u), 4)
+            count[toks[0]] += 1
+        assert np.abs(count / len(grid) - p).max() <= 2 / len(grid)   # each interval's ends cut at most two grid cells
+
+
+def test_accept_sample_limits_and_faults():
+    x = np.zeros((3, 4))
+    par, tok = [-1, 0, 1], [0, 1, 2]
+    assert T.accept_sample(par, tok, 3, x, 1.0, np.zeros(3), 1) == ([0, 1], [1, 0])       # P = 1: one draft
+    assert T.accept_sample(par, tok, 2, x, 1.0, np.zeros(3), 4) == ([0, 1], [1, 0])       # slot 2 not in use
+    assert T.accept_sample(par, tok, 3, x, 0.0, np.zeros(3), 4) == ([0], [0])             # greedy: lowest index
+    bad = x.copy()
+    bad[1, 3] = np.nan
+    assert T.accept_sample(par, tok, 3, bad, 1.0, np.zeros(3), 4) == ([0, 1], [1, -1])
+    masked = np.full((3, 4), -np.inf)
+    assert T.accept_sample(par, tok, 3, masked, 1.0, np.zeros(3), 4) == ([0], [-1])
+    masked[0, 1] = 0.0
+    assert T.accept_sample(par, tok, 3, masked, 1.0, np.full(3, 0.999), 4) == ([0, 1], [1, -1])
+    assert T.accept_sample(par, tok, 3, x, -1.0, np.zeros(3), 4) == ([0], [-1])

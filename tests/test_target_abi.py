@@ -1,0 +1,135 @@
+"""libgdntree_target.so loads, exports what its header declares, and refuses bad arguments on the
+host before touching a device (CPU only: no compute call is made)."""
+import os
+import re
+import subprocess
+
+import pytest
+import torch
+
+import gdn_draft_tree_amd as g
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "gdntree_target.h")
+FAKE = 0x1000  # never dereferenced: every case below fails validation first
+L = g.TARGET_LIB
+
+
+def test_library_exports_what_the_header_declares():
+    src = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    declared = set(re.findall(r"\b(gdntree_[a-z_]+)\s*\(", src))
+    out = subprocess.run(["nm", "-D", "--defined-only", g.TARGET_LIB_PATH], capture_output=True, text=True, check=True)
+    assert set(re.findall(r"\bT (gdntree_\w+)", out.stdout)) == declared == set(g.TARGET_EXPORTED)
+
+
+def cache(**kw):
+    f = dict(k=FAKE, v=FAKE, k_scale=FAKE, v_scale=FAKE, L=2, pages=8, H_kv=4, page_size=16, d=128, dtype=1)
+    f.update(kw)
+    return g.CCache(*[f[n] for n, _ in g.CCache._fields_])
+
+
+CACHE_CASES = [
+    (dict(k=None), 1), (dict(v=None), 1), (dict(k_scale=None), 1), (dict(v_scale=None), 1), (dict(dtype=2), 1),
+    (dict(k=FAKE + 8), 1), (dict(v=FAKE + 4), 1), (dict(k_scale=FAKE + 1), 1), (dict(L=0), 1), (dict(pages=0), 1),
+    (dict(H_kv=0), 1), (dict(page_size=0), 1), (dict(d=0), 1), (dict(page_size=8), 2), (dict(page_size=48), 2),
+    (dict(page_size=512), 2), (dict(d=96), 2), (dict(d=256), 2),
+]
+
+
+@pytest.mark.parametrize("kw,expect", CACHE_CASES)
+def test_bad_caches_are_refused(kw, expect):
+    c = cache(**kw)
+    assert L.gdntree_cache_write(c, 0, FAKE, 4, FAKE, FAKE, 2, 3, 1, FAKE, FAKE, None) == expect
+    assert L.gdntree_cache_read(c, 0, FAKE, 4, FAKE, FAKE, 2, 3, 1, FAKE, FAKE, None) == expect
+    assert L.gdntree_cache_commit(c, FAKE, 4, FAKE, 2, 24, 8, FAKE, FAKE, None) == expect
+    assert L.gdntree_attend(c, 0, FAKE, 4, FAKE, FAKE, FAKE, 2, 3, 8, 1, FAKE, 0.1, FAKE, FAKE, 1 << 40, None) == expect
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(table=None), 1), (dict(width=0), 1), (dict(start=None), 1), (dict(k=None), 1), (dict(v=None), 1),
+    (dict(k=FAKE + 2), 1), (dict(layer=-1), 1), (dict(layer=2), 1), (dict(B=0), 1), (dict(R=0), 1), (dict(dt=7), 1),
+    (dict(B=1 << 30, R=1 << 30), 2),
+])
+def test_rows_calls_refuse(kw, expect):
+    a = dict(layer=0, table=FAKE, width=4, start=FAKE, B=2, R=3, dt=1, k=FAKE, v=FAKE)
+    a.update(kw)
+    for fn in (L.gdntree_cache_write, L.gdntree_cache_read):
+        assert fn(cache(), a["layer"], a["table"], a["width"], a["start"], None, a["B"], a["R"], a["dt"], a["k"],
+                  a["v"], None) == expect
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(table=None), 1), (dict(ctx=None), 1), (dict(acc_len=None), 1), (dict(acc_node=None), 1), (dict(B=0), 1),
+    (dict(N=0), 1), (dict(P=0), 1), (dict(N=65), 2), (dict(P=17), 2), (dict(B=1 << 29), 2),
+])
+def test_cache_commit_refuses(kw, expect):
+    a = dict(table=FAKE, ctx=FAKE, B=2, N=24, P=8, acc_len=FAKE, acc_node=FAKE)
+    a.update(kw)
+    assert L.gdntree_cache_commit(cache(), a["table"], 4, a["ctx"], a["B"], a["N"], a["P"], a["acc_len"],
+                                  a["acc_node"], None) == expect
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(ctx=None), 1), (dict(q=None), 1), (dict(o=None), 1), (dict(ws=None), 1), (dict(q=FAKE + 8), 1),
+    (dict(o=FAKE + 2), 1), (dict(ws=FAKE + 4), 1), (dict(layer=2), 1), (dict(B=0), 1), (dict(R=0), 1), (dict(Hq=0), 1),
+    (dict(dt=5), 1), (dict(scale=0.0), 1), (dict(scale=-1.0), 1), (dict(scale=float("nan")), 1),
+    (dict(scale=float("inf")), 1), (dict(size=16), 1), (dict(R=66), 2), (dict(Hq=6), 2), (dict(Hq=68), 2),
+    (dict(B=(1 << 31) - 1), 2),
+])
+def test_attend_refuses(kw, expect):
+    a = dict(layer=0, ctx=FAKE, B=2, R=3, Hq=8, dt=1, q=FAKE, scale=0.1, o=FAKE, ws=FAKE, size=1 << 40)
+    a.update(kw)
+    assert L.gdntree_attend(cache(), a["layer"], FAKE, 4, a["ctx"], None, None, a["B"], a["R"], a["Hq"], a["dt"],
+                            a["q"], a["scale"], a["o"], a["ws"], a["size"], None) == expect
+
+
+def test_workspace_sizes():
+    assert L.gdntree_attend_workspace(2, 66, 8, 4, 128) == 0 and L.gdntree_attend_workspace(2, 3, 6, 4, 128) == 0
+    assert L.gdntree_attend_workspace(0, 3, 8, 4, 128) == 0
+    assert 0 < L.gdntree_attend_workspace(1, 1, 8, 8, 64) < L.gdntree_attend_workspace(1, 65, 8, 8, 128) < 1 << 28
+    assert L.gdntree_accept_sample_workspace(1, 65, 100) == 0
+    assert L.gdntree_accept_sample_workspace(1, 64, (1 << 24) + 1) == 0
+    assert 0 < L.gdntree_accept_sample_workspace(1, 1, 1) < L.gdntree_accept_sample_workspace(32, 64, 151936) < 1 << 22
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(parent=None), 1), (dict(token=None), 1), (dict(n_nodes=None), 1), (dict(logits=None), 1),
+    (dict(logits=FAKE + 1), 1), (dict(temp=None), 1), (dict(uni=None), 1), (dict(acc=(None, FAKE, FAKE)), 1),
+    (dict(acc=(FAKE, FAKE, None)), 1), (dict(ws=None), 1), (dict(ws=FAKE + 8), 1), (dict(B=0), 1), (dict(N=0), 1),
+    (dict(P=0), 1), (dict(V=0), 1), (dict(dt=3), 1), (dict(size=64), 1), (dict(N=65), 2), (dict(P=17), 2),
+    (dict(V=(1 << 24) + 1), 2), (dict(B=1 << 30), 2),
+])
+def test_accept_sample_refuses(kw, expect):
+    a = dict(parent=FAKE, token=FAKE, n_nodes=FAKE, B=2, N=24, P=8, V=1000, dt=1, logits=FAKE, temp=FAKE, uni=FAKE,
+             acc=(FAKE, FAKE, FAKE), ws=FAKE, size=1 << 40)
+    a.update(kw)
+    tree = g.CTree(a["parent"], None, None, a["token"], None, None, a["n_nodes"])
+    assert L.gdntree_accept_sample(tree, a["B"], a["N"], a["P"], a["V"], a["dt"], a["logits"], a["temp"], a["uni"],
+                                   *a["acc"], a["ws"], a["size"], None) == expect
+
+
+def test_no_device_is_reported():
+    if torch.cuda.is_available():
+        pytest.skip("there is a device")
+    assert L.gdntree_cache_write(cache(), 0, FAKE, 4, FAKE, FAKE, 2, 3, 1, FAKE, FAKE, None) == g.GDNTREE_ERR_DEVICE
+    assert L.gdntree_attend(cache(), 0, FAKE, 4, FAKE, None, None, 2, 3, 8, 1, FAKE, 0.1, FAKE, FAKE, 1 << 40,
+                            None) == g.GDNTREE_ERR_DEVICE
+
+
+def test_binding_refuses_host_tensors_and_bad_caches():
+    rows = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16)
+    i32 = torch.zeros(1, dtype=torch.int32)
+    kv = g.KVCache.empty(1, 4, 4, 16, 64, device="cpu")
+    table = torch.zeros(1, 4, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        g.gdntree_cache_write(kv, 0, table, i32, rows, rows)
+    with pytest.raises(ValueError):
+        g.gdntree_cache_read(kv, 0, table, i32, 2)
+    with pytest.raises(ValueError):
+        g.gdntree_attend(rows, kv, 0, table, i32)
+    with pytest.raises(ValueError):
+        g.gdntree_cache_commit(kv, table, i32, i32, torch.zeros(1, 5, dtype=torch.int32), 4)
+    with pytest.raises(ValueError):
+        g.gdntree_accept_sample(None, torch.zeros(1, 5, 9), torch.ones(1), torch.zeros(1, 5), 4)
+    with pytest.raises(ValueError):
+        g.KVCache.empty(1, 4, 4, 16, 64, dtype=torch.float16, device="cpu")
