@@ -8,15 +8,19 @@
 // of w over the vocabulary without the children first exceeds U Z - sum w(c_i).
 //
 // Which rows the walk visits is known only once their parents' are read, so every used row is
-// read once, at full bandwidth, by a first kernel (it is bound by HBM: one fp32 exponential per
-// logit); the rest is latency.  Three kernels on the stream:
-//  1. sample_stats_kernel: workgroup (chunk, row) reduces up to kChunkGroups pieces of 8192 logits
-//     to their maximum and the sum of fp32 exponentials (a greedy request: the maximum and its
-//     lowest index).  At most kMaxChunks chunks a row, however long the vocabulary is.
-//  2. sample_walk_kernel: every workgroup of a request does the walk (one wave, the statistics and
-//     the children's logits staged in LDS by one round of loads), then sums its part of the last
-//     node's row without the children, in fp64.
-//  3. sample_pick_kernel: finds the part, then the token, by fp64 prefix sums.
+// read once, at full bandwidth, by a first kernel (bound by HBM and, close behind, by one fp32
+// exponential per logit); the rest is latency.  Three kernels on the stream:
+//  1. sample_stats_kernel: workgroup (chunk, row) reduces up to stat_pieces() pieces of 8192
+//     logits to their maximum and the sum of fp32 exponentials (a greedy request: the maximum and
+//     its lowest index).  At most kMaxChunks chunks a row, however long the vocabulary is.
+//  2. sample_walk_kernel: every workgroup of a request stages the statistics and the drafted
+//     tokens' logits in LDS by one round of loads, finds for every node at once which child its
+//     random number takes (one lane per node: the walk itself is then a chase of at most 17
+//     links), and sums its part of the last node's row without the children, in fp64.
+//  3. sample_pick_kernel: one workgroup a request finds the part, then the token, by fp64 prefix
+//     sums.  (Left to the request's last workgroup of kernel 2, behind a counter, it took longer:
+//     every workgroup's release at device scope writes its L2 back, 58 us against 24 + 12 us for
+//     32 requests.)
 // The bonus token's place among 10^5 tokens is what needs fp64: the borders between tokens lie
 // 10^-6 and less apart, and an fp32 sum would put a random number on the wrong side of one about
 // once in a hundred draws.  A child's interval is held to the fp32 statistics (1e-7).
@@ -30,28 +34,39 @@ typedef unsigned long long u64;
 
 constexpr int kPiece = 8192;       // logits one workgroup of 256 lanes holds in registers
 constexpr int kMaxChunks = 32;     // statistics per row
+constexpr int kStatGroups = 4096;  // two rounds of eight workgroups per CU
 constexpr int kPart = 4096;        // logits per fp64 partial sum: 16 per lane
 constexpr float kNegInf = -__builtin_inff();
 
-__host__ __device__ inline int stat_pieces(int V) { return (V + 7 + kPiece * kMaxChunks - 1) / (kPiece * kMaxChunks); }
-__host__ __device__ inline int stat_chunks(int V) {
-  const int per = kPiece * stat_pieces(V);
+// Pieces per chunk: as many as leave kStatGroups workgroups for the batch (longer runs keep the
+// next piece's loads in flight behind the present one's arithmetic), and few enough chunks a row.
+__host__ __device__ inline int stat_pieces(long long rows, int V) {
+  const int row = (V + 7 + kPiece - 1) / kPiece;
+  const long long fill = rows * row / kStatGroups;
+  const int least = (row + kMaxChunks - 1) / kMaxChunks;
+  return fill > row ? row : fill > least ? (int)fill : least;
+}
+__host__ __device__ inline int stat_chunks(long long rows, int V) {
+  const int per = kPiece * stat_pieces(rows, V);
   return (V + 7 + per - 1) / per;
 }
 __host__ __device__ inline int sum_parts(int V) { return (V + kPart - 1) / kPart; }
 
+// With c = log2(e) / T in fp32: the sum is of exp2(l c - r), r = fl(m c), so that an exponent is one
+// fused multiply-add, rounded once.  r is not m c, but it is known: joining sums takes
+// exp2(r - c max m), the difference in fp64.  (Where m c overflows, r is m c itself.)
 struct Stat {
   float m;      // maximum
-  unsigned s;   // fp32 bits of the sum of exp2((l - m) log2(e) / T); greedy: lowest index of the maximum
+  unsigned s;   // fp32 bits of the sum; greedy: lowest index of the maximum
 };
 
 // What kernel 2 leaves for kernel 3.
 struct Pending {
-  double u, children;  // the node's random number; sum of w over its children's tokens
-  float top;           // the node's largest logit
-  int node;            // -1: nothing left to draw
-  int len;             // tau
-  int kids;            // whether the children were candidates
+  double u, kept;  // the last node's random number; its children's weight
+  float top;       // its largest logit
+  int node;        // -1: the bonus is known
+  int len;         // tau
+  int kids;        // whether the node's children were candidates
 };
 
 struct Workspace {
@@ -66,7 +81,7 @@ __host__ __device__ inline Workspace carve(void *ws, int B, int R, int V) {
   unsigned char *at = static_cast<unsigned char *>(ws);
   Workspace w;
   w.stat = reinterpret_cast<Stat *>(at);
-  at += round16((size_t)B * R * stat_chunks(V) * sizeof(Stat));
+  at += round16((size_t)B * R * stat_chunks((long long)B * R, V) * sizeof(Stat));
   w.part = reinterpret_cast<double *>(at);
   at += round16((size_t)B * sum_parts(V) * sizeof(double));
   w.pend = reinterpret_cast<Pending *>(at);
@@ -104,11 +119,52 @@ __device__ __forceinline__ bool temperature_ok(float t) { return t >= 0.f && t <
 // log2(e) / T, kept finite (a product with 0 is then 0)
 __device__ __forceinline__ float inverse_log2(float t) { return fminf(1.4426950408889634f / t, 3.0e38f); }
 
+__device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
+
+// c * (reference of maximum m) - c * (maximum top), in log2
+__device__ __forceinline__ float rebase(float m, float top, float c) {
+  const float r = m * c;
+  return (float)((finite(r) ? (double)r : (double)m * c) - (double)top * c);
+}
+
+// Eight logits as they are stored: one 16-byte load (bf16) or two.
+template <bool BF16>
+struct Raw8 {
+  u32x4 w[BF16 ? 1 : 2];
+  __device__ __forceinline__ float operator[](int i) const {
+    if constexpr (BF16) return __uint_as_float(i & 1 ? w[0][i >> 1] & 0xffff0000u : w[0][i >> 1] << 16);
+    else return __uint_as_float(w[i >> 2][i & 3]);
+  }
+};
+
+// Elements e .. e + 7 of a padded row; those outside [pad, end) are -inf.
+template <bool BF16>
+__device__ __forceinline__ Raw8<BF16> load_raw8(const unsigned char *base, int e, int pad, int end) {
+  constexpr int ES = BF16 ? 2 : 4;
+  Raw8<BF16> r;
+  if (e >= pad && e + 8 <= end) {
+    r.w[0] = *reinterpret_cast<const u32x4 *>(base + (size_t)e * ES);
+    if constexpr (!BF16) r.w[1] = *reinterpret_cast<const u32x4 *>(base + (size_t)e * ES + 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bool in = e + i >= pad && e + i < end;
+      if constexpr (BF16) {
+        const unsigned h = in ? reinterpret_cast<const uint16_t *>(base)[e + i] : 0xff80u;
+        r.w[0][i >> 1] = i & 1 ? r.w[0][i >> 1] | h << 16 : h;
+      } else {
+        r.w[i >> 2][i & 3] = in ? reinterpret_cast<const unsigned *>(base)[e + i] : 0xff800000u;
+      }
+    }
+  }
+  return r;
+}
+
 template <bool BF16>
 __global__ __launch_bounds__(256) void sample_stats_kernel(SampleParams p, Workspace ws) {
   __shared__ float s_m[4], s_s[4];
   __shared__ unsigned s_i[4];
-  const int nc = stat_chunks(p.V), pieces = stat_pieces(p.V);
+  const int nc = stat_chunks(p.B * p.R, p.V), pieces = stat_pieces(p.B * p.R, p.V);
   const int chunk = blockIdx.x % nc, row = blockIdx.x / nc;
   const int b = row / p.R, t = row - b * p.R;
   const int n = p.n_nodes[b];
@@ -122,35 +178,22 @@ __global__ __launch_bounds__(256) void sample_stats_kernel(SampleParams p, Works
   // element 0 of the row sits `pad` elements behind a 16-byte boundary: pieces are cut at boundaries
   constexpr int ES = BF16 ? 2 : 4;
   const unsigned char *base = static_cast<const unsigned char *>(p.logits) + (size_t)row * p.V * ES;
-  const int pad = (int)((reinterpret_cast<uintptr_t>(base) & 15) / ES);
+  const int pad = (int)((reinterpret_cast<uintptr_t>(base) & 15) / ES), end = p.V + pad;
   base -= (size_t)pad * ES;
 
   float m_run = kNegInf, s_run = 0.f;
   unsigned i_run = 0xffffffffu;
-  for (int piece = 0; piece < pieces; ++piece) {
-    const int first = (chunk * pieces + piece) * kPiece;  // in padded elements
-    if (first >= p.V + pad) break;
+  const int first0 = chunk * pieces * kPiece, last = min(end, first0 + pieces * kPiece);
+  Raw8<BF16> next[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) next[q] = load_raw8<BF16>(base, first0 + 8 * (tid + 256 * q), pad, end);
+  for (int first = first0; first < last; first += kPiece) {
     float x[32];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int e = first + 8 * (tid + 256 * q);
-      if (e >= pad && e + 8 <= p.V + pad) {
-        if constexpr (BF16) {
-          const u16x8 h = *reinterpret_cast<const u16x8 *>(base + (size_t)e * 2);
+    for (int i = 0; i < 32; ++i) x[i] = next[i >> 3][i & 7];
+    if (first + kPiece < last)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[8 * q + i] = bf16_bits_to_f32(h[i]);
-        } else {
-          const f32x4 a = *reinterpret_cast<const f32x4 *>(base + (size_t)e * 4);
-          const f32x4 d = *reinterpret_cast<const f32x4 *>(base + (size_t)e * 4 + 16);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) { x[8 * q + i] = a[i]; x[8 * q + 4 + i] = d[i]; }
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          x[8 * q + i] = e + i >= pad && e + i < p.V + pad ? logit<BF16>(base, (size_t)(e + i)) : kNegInf;
-      }
-    }
+      for (int q = 0; q < 4; ++q) next[q] = load_raw8<BF16>(base, first + kPiece + 8 * (tid + 256 * q), pad, end);
     float m = x[0];
 #pragma unroll
     for (int i = 1; i < 32; ++i) m = fmaxf(m, x[i]);
@@ -166,23 +209,34 @@ __global__ __launch_bounds__(256) void sample_stats_kernel(SampleParams p, Works
       idx = wave_min(m == kNegInf ? 0xffffffffu : idx);
       if (m > m_run) { m_run = m; i_run = idx; }  // pieces come in order: the first stays on a tie
       if (__any(nan)) s_run = __builtin_nanf("");
-    } else {
-      const float m_new = fmaxf(m_run, m);
-      if (m_new > kNegInf) {
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) s += __builtin_amdgcn_exp2f((x[i] - m_new) * c);
-        s = wave_add(s);
-        s_run = (m_run == kNegInf ? 0.f : s_run * __builtin_amdgcn_exp2f((m_run - m_new) * c)) + s;
-        m_run = m_new;
-      } else {
-        bool nan = false;  // nothing but -inf and NaN so far
-#pragma unroll
-        for (int i = 0; i < 32; ++i) nan = nan || x[i] != x[i];
-        if (__any(nan)) s_run = __builtin_nanf("");
-      }
+      continue;
     }
+    const float m_new = fmaxf(m_run, m);
+    if (m_new == kNegInf) {  // nothing but -inf and NaN so far
+      bool nan = false;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) nan = nan || x[i] != x[i];
+      if (__any(nan)) s_run = __builtin_nanf("");
+      continue;
+    }
+    const float r = m_new * c;
+    float s0 = 0.f, s1 = 0.f;
+    if (finite(r)) {
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        s0 += __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], c, -r));
+        s1 += __builtin_amdgcn_exp2f(__builtin_fmaf(x[i + 1], c, -r));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) s0 += __builtin_amdgcn_exp2f((x[i] - m_new) * c);
+    }
+    // lanes keep sums of their own; they are joined once, below
+    if (m_run != m_new) s_run = m_run == kNegInf ? s_run : s_run * __builtin_amdgcn_exp2f(rebase(m_run, m_new, c) - rebase(m_new, m_new, c));
+    s_run += s0 + s1;
+    m_run = m_new;
   }
+  if (!greedy) s_run = wave_add(s_run);
   if (lane == 0) { s_m[wave] = m_run; s_s[wave] = s_run; s_i[wave] = i_run; }
   __syncthreads();
   if (tid == 0) {
@@ -192,7 +246,8 @@ __global__ __launch_bounds__(256) void sample_stats_kernel(SampleParams p, Works
     for (int w = 0; w < 4; ++w) {
       if (s_m[w] == m) idx = min(idx, s_i[w]);
       // a NaN sum stays one; a wave of -inf alone adds nothing
-      s += s_m[w] == kNegInf || greedy ? s_s[w] : s_s[w] * __builtin_amdgcn_exp2f((s_m[w] - m) * c);
+      s += s_m[w] == kNegInf || greedy ? s_s[w]
+                                       : s_s[w] * __builtin_amdgcn_exp2f(rebase(s_m[w], m, c) - rebase(m, m, c));
     }
     Stat st;
     st.m = s != s ? __builtin_nanf("") : m;  // the row holds a NaN
@@ -201,141 +256,180 @@ __global__ __launch_bounds__(256) void sample_stats_kernel(SampleParams p, Works
   }
 }
 
-// The tokens of the children of `node` in slots < n, as bits of one part of the vocabulary.
-__device__ __forceinline__ void mark_children(const SampleParams &p, int b, int n, int node, int first, u64 *bits,
-                                              int tid, int threads) {
-  for (int i = tid; i < kPart / 64; i += threads) bits[i] = 0;
+// The tokens of the children of `node` among the slots 1 .. n - 1 (in LDS), as bits of one part of
+// the vocabulary.
+__device__ __forceinline__ void mark_children(const int *par, const int *tok, int n, int node, int first, u64 *bits,
+                                              int tid) {
   __syncthreads();
-  for (int t = 1 + tid; t < n; t += threads) {
-    const unsigned at = (unsigned)p.token[(size_t)b * p.R + t] - (unsigned)first;
-    if (p.parent[(size_t)b * p.R + t] == node && at < (unsigned)kPart) atomicOr(&bits[at >> 6], 1ull << (at & 63));
+  if (tid < kPart / 64) bits[tid] = 0;
+  __syncthreads();
+  if (tid >= 1 && tid < n && par[tid] == node) {
+    const unsigned at = (unsigned)tok[tid] - (unsigned)first;
+    if (at < (unsigned)kPart) atomicOr(&bits[at >> 6], 1ull << (at & 63));
   }
   __syncthreads();
 }
 
+// exp(x) for x <= 0, from the series of e^r on |r| <= ln(2) / 2 (the first term left out is
+// r^12 / 12!, 6e-15) and a power of two; 0 below 2^-1021.
+__device__ __forceinline__ double exp_neg(double x) {
+  const double y = fmax(x * 1.4426950408889634074, -1100.0);
+  const double k = rint(y), r = (y - k) * 0.69314718055994530942;
+  double e = 1.0 / 39916800.0;
+  e = fma(e, r, 1.0 / 3628800.0);
+  e = fma(e, r, 1.0 / 362880.0);
+  e = fma(e, r, 1.0 / 40320.0);
+  e = fma(e, r, 1.0 / 5040.0);
+  e = fma(e, r, 1.0 / 720.0);
+  e = fma(e, r, 1.0 / 120.0);
+  e = fma(e, r, 1.0 / 24.0);
+  e = fma(e, r, 1.0 / 6.0);
+  e = fma(e, r, 0.5);
+  e = fma(e, r, 1.0);
+  e = fma(e, r, 1.0);
+  const int n = (int)k;
+  return n < -1021 ? 0.0 : __longlong_as_double(__double_as_longlong(e) + ((long long)n << 52));
+}
+
 // The fp64 weights of this lane's 16 tokens of a part; children and tokens past V weigh nothing.
+// inv: 1 / T.
 template <bool BF16>
 __device__ __forceinline__ void weights16(const SampleParams &p, size_t row, int first, const u64 *bits, float top,
-                                          double temp, int tid, double w[16]) {
+                                          double inv, int tid, double w[16]) {
+  float l[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i)  // in bounds whatever the place, so that all loads are in flight at once
+    l[i] = logit<BF16>(p.logits, row * p.V + min(first + 16 * tid + i, p.V - 1));
   const unsigned out = (unsigned)(bits[tid >> 2] >> (16 * (tid & 3))) & 0xffffu;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const int x = first + 16 * tid + i;
-    w[i] = 0.0;
-    if (x < p.V && !((out >> i) & 1)) {
-      const float l = logit<BF16>(p.logits, row * p.V + x);
-      w[i] = exp(((double)l - (double)top) / temp);
-    }
+    const double x = exp_neg(((double)l[i] - (double)top) * inv);
+    w[i] = first + 16 * tid + i < p.V && !((out >> i) & 1) ? x : 0.0;
   }
 }
 
 template <bool BF16>
 __global__ __launch_bounds__(256) void sample_walk_kernel(SampleParams p, Workspace ws) {
   __shared__ Stat s_stat[kMaxSlots * kMaxChunks];
-  __shared__ float s_logit[kMaxSlots];
-  __shared__ int s_par[kMaxSlots], s_tok[kMaxSlots], s_path[kMaxAnc];
-  __shared__ Pending s_pend;
-  __shared__ int s_bonus;
+  __shared__ double s_at[kMaxSlots], s_w[kMaxSlots];  // random number times normaliser; a draft's weight
+  __shared__ float s_top[kMaxSlots];                  // largest logit; NaN: no distribution
+  __shared__ int s_best[kMaxSlots], s_next[kMaxSlots], s_path[kMaxAnc];
+  __shared__ int s_par[kMaxSlots], s_tok[kMaxSlots];
   __shared__ u64 s_bits[kPart / 64];
-  __shared__ double s_sum[4];
+  __shared__ double s_sum[4], s_uni[kMaxSlots];
+  __shared__ u64 s_kids[kMaxSlots];                   // bit t - 1: slot t is a child
+  __shared__ int s_len, s_last_node;
   const int parts = sum_parts(p.V);
   const int b = blockIdx.x / parts, part = blockIdx.x - b * parts;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int nc = stat_chunks(p.B * p.R, p.V);
+  const size_t row0 = (size_t)b * p.R;
+  // every load that needs no other first (slots not in use are read and dropped)
   const int n = p.n_nodes[b];
-  if (n < 1 || n > p.R) return;
-  const int nc = stat_chunks(p.V);
   const float temp = p.temperature[b];
+  int par = -1, tok = -1;
+  double uni = 0.0;
+  if (tid < p.R) {
+    par = p.parent[row0 + tid];
+    tok = p.token[row0 + tid];
+    uni = p.uniform[row0 + tid];
+  }
+  for (int i = tid; i < p.R * nc; i += 256) s_stat[i] = ws.stat[row0 * nc + i];
+  if (n < 1 || n > p.R) return;
   const bool t_ok = temperature_ok(temp), greedy = temp == 0.f;
-  if (t_ok)
-    for (int i = tid; i < n * nc; i += 256) s_stat[i] = ws.stat[(size_t)b * p.R * nc + i];
-  if (tid < n) {
-    const int par = tid ? p.parent[(size_t)b * p.R + tid] : -1, tok = p.token[(size_t)b * p.R + tid];
+  const float c = inverse_log2(temp);
+  float mine = kNegInf;  // the slot's token's logit under its parent; without one it has no mass
+  if (tid < p.R) {
+    if (tid == 0 || tid >= n || par < 0 || par >= n) par = -1;
+    if (par >= 0 && tok >= 0 && tok < p.V) mine = logit<BF16>(p.logits, (row0 + par) * p.V + tok);
     s_par[tid] = par;
     s_tok[tid] = tok;
-    // a child's logit under its parent; outside the vocabulary or without a parent: no mass
-    s_logit[tid] = par >= 0 && par < n && tok >= 0 && tok < p.V
-                       ? logit<BF16>(p.logits, ((size_t)b * p.R + par) * p.V + tok) : kNegInf;
+    s_uni[tid] = uni;
+    s_next[tid] = 0x7fffffff;
+    s_kids[tid] = 0;
   }
   __syncthreads();
+  if (tid < n && par >= 0) atomicOr(&s_kids[par], 1ull << (tid - 1));
 
-  if (wave == 0) {
-    const double *uni = p.uniform + (size_t)b * p.R;
-    int u = 0, len = 1, bonus = -1;
-    Pending pend{0.0, 0.0, 0.f, -1, 0, 0};
-    if (lane == 0) s_path[0] = 0;
-    while (t_ok) {
-      // the row's maximum and normaliser
-      const Stat st = lane < nc ? s_stat[u * nc + lane] : Stat{kNegInf, greedy ? 0xffffffffu : 0u};
-      const float top = wave_max(st.m);
-      if (__any(st.m != st.m) || top == kNegInf || top == __builtin_inff()) break;  // no distribution
-      const bool more = len <= p.P;
-      // lane l has slot l, and lane 0 slot 64 as well (the last one)
-      const bool kid0 = more && lane >= 1 && lane < n && s_par[lane] == u;
-      const bool kid1 = more && lane == 0 && n > 64 && s_par[64] == u;
-      const int tok0 = lane < n ? s_tok[lane] : -1, tok1 = n > 64 ? s_tok[64] : -1;
-      int next = -1;
-      if (greedy) {
-        const unsigned best = wave_min(st.m == top ? st.s : 0xffffffffu);
-        const u64 hit = __ballot(kid0 && tok0 == (int)best);
-        if (hit) next = __ffsll((long long)hit) - 1;
-        else if (__any(kid1 && tok1 == (int)best)) next = 64;
-        if (next < 0) { bonus = (int)best; break; }
-      } else {
-        const double z = wave_add(st.m == kNegInf ? 0.0 : (double)__uint_as_float(st.s) *
-                                                              exp(((double)st.m - (double)top) / (double)temp));
-        // weights of the children, nothing for one that repeats an earlier sibling's token
-        bool dup0 = false, dup1 = false;
-        for (u64 rest = __ballot(kid0); rest; rest &= rest - 1) {
-          const int s = __ffsll((long long)rest) - 1, ts = __builtin_amdgcn_readlane(tok0, s);
-          dup0 = dup0 || (s < lane && ts == tok0);
-          dup1 = dup1 || ts == tok1;
-        }
-        const double w0 = kid0 && !dup0 ? exp(((double)s_logit[lane] - (double)top) / (double)temp) : 0.0;
-        const double w1 = kid1 && !dup1 ? exp(((double)s_logit[64] - (double)top) / (double)temp) : 0.0;
-        double end = w0;  // running sum in slot order
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-          const double y = __shfl_up(end, o);
-          if (lane >= o) end += y;
-        }
-        const double all0 = __shfl(end, 63), last1 = __shfl(w1, 0);
-        const double at = uni[u] * z;
-        const u64 hit = __ballot(kid0 && at >= end - w0 && at < end);
-        if (hit) next = __ffsll((long long)hit) - 1;
-        else if (__any(kid1 && at >= all0 && at < all0 + w1)) next = 64;
-        if (next < 0) {
-          pend = Pending{uni[u], all0 + last1, top, u, len, more ? 1 : 0};
-          break;
-        }
-      }
-      u = next;
-      if (lane == 0) s_path[len] = u;
-      ++len;
+  // one lane per node: its row's maximum, normaliser, and (greedy) the lowest index of the maximum
+  if (tid < n && t_ok) {
+    const Stat *st = s_stat + tid * nc;
+    float top = kNegInf;
+    bool ok = true;
+    unsigned best = 0xffffffffu;
+    for (int i = 0; i < nc; ++i) {
+      ok = ok && st[i].m == st[i].m;
+      if (st[i].m > top) { top = st[i].m; best = st[i].s; }  // chunks come in order
     }
-    if (lane == 0) {
-      pend.len = len;
-      s_pend = pend;
-      s_bonus = bonus;
-    }
+    ok = ok && top > kNegInf && top < __builtin_inff();
+    double z = 0.0;
+    if (!greedy)
+      for (int i = 0; i < nc; ++i)
+        if (st[i].m > kNegInf) z += (double)__uint_as_float(st[i].s) * (double)__builtin_amdgcn_exp2f(rebase(st[i].m, top, c));
+    s_top[tid] = ok ? top : __builtin_nanf("");
+    s_at[tid] = uni * z;
+    s_best[tid] = (int)best;
   }
   __syncthreads();
-  const Pending pend = s_pend;
-  if (part == 0) {
-    if (tid <= p.P) {
-      const size_t ab = (size_t)b * (p.P + 1);
-      const int len = pend.len;
-      if (tid == 0) p.acc_len[b] = len;
-      p.acc_node[ab + tid] = tid < len ? s_path[tid] : -1;
-      // a pending bonus is written by the pick
-      p.acc_tok[ab + tid] = tid < len - 1 ? s_tok[s_path[tid + 1]] : tid == len - 1 ? s_bonus : -1;
-    }
-    if (tid == 0) ws.pend[b] = pend;
+  // a draft's earlier siblings: bit s - 1 for slot s
+  const u64 elder = tid < n && par >= 0 ? s_kids[par] & ((1ull << (tid - 1)) - 1) : 0;
+  // one lane per draft: its weight (a token that an earlier sibling has weighs nothing), then
+  // whether it is the child its parent's random number takes
+  if (tid < n && t_ok) {
+    bool repeat = false;
+    for (u64 e = elder; e; e &= e - 1) repeat = repeat || s_tok[__ffsll((long long)e)] == tok;
+    s_w[tid] = mine == kNegInf || greedy || repeat ? 0.0 : exp_neg(((double)mine - (double)s_top[par]) / (double)temp);
   }
-  if (pend.node < 0) return;
+  __syncthreads();
+  if (tid < n && t_ok && par >= 0) {  // a node without a distribution takes nothing (NaN compares false)
+    bool taken;
+    if (greedy) {
+      taken = tok == s_best[par] && s_top[par] == s_top[par];
+    } else {
+      double before = 0.0;
+      for (u64 e = elder; e; e &= e - 1) before += s_w[__ffsll((long long)e)];
+      taken = s_at[par] >= before && s_at[par] < before + s_w[tid] && s_top[par] == s_top[par];
+    }
+    if (taken) atomicMin(&s_next[par], tid);  // greedy siblings may share the token: the lowest slot
+  }
+  __syncthreads();
+  if (tid == 0) {
+    int u = 0, len = 1;
+    s_path[0] = 0;
+    while (t_ok && len <= p.P && s_next[u] < n) {
+      u = s_next[u];
+      s_path[len++] = u;
+    }
+    s_len = len;
+    s_last_node = u;
+  }
+  __syncthreads();
+  const int len = s_len, node = s_last_node;
+  const bool kids = len <= p.P;                          // the node's children were candidates
+  const bool ok = t_ok && s_top[node] == s_top[node];    // there is a bonus to emit
+  if (part == 0 && tid <= p.P) {
+    const size_t ab = (size_t)b * (p.P + 1);
+    if (tid == 0) p.acc_len[b] = len;
+    p.acc_node[ab + tid] = tid < len ? s_path[tid] : -1;
+    // a drawn bonus is written by the next kernel
+    if (tid != len - 1 || !ok || greedy)
+      p.acc_tok[ab + tid] = tid < len - 1 ? s_tok[s_path[tid + 1]] : tid == len - 1 && ok ? s_best[node] : -1;
+  }
+  const bool draw = ok && !greedy;
+  const float top = s_top[node];
+  if (part == 0 && wave == 0) {
+    double kept = 0.0;
+    if (draw && kids && lane >= 1 && lane < n && s_par[lane] == node) kept = s_w[lane];
+    if (draw && kids && lane == 0 && n > 64 && s_par[64] == node) kept = s_w[64];
+    kept = wave_add(kept);
+    if (lane == 0) ws.pend[b] = Pending{draw ? s_uni[node] : 0.0, kept, top, draw ? node : -1, len, kids};
+  }
+  if (!draw) return;
+
   const int first = part * kPart;
-  mark_children(p, b, pend.kids ? n : 0, pend.node, first, s_bits, tid, 256);
+  mark_children(s_par, s_tok, kids ? n : 0, node, first, s_bits, tid);
   double w[16], sum = 0.0;
-  weights16<BF16>(p, (size_t)b * p.R + pend.node, first, s_bits, pend.top, (double)temp, tid, w);
+  weights16<BF16>(p, row0 + node, first, s_bits, top, 1.0 / (double)temp, tid, w);
 #pragma unroll
   for (int i = 0; i < 16; ++i) sum += w[i];
   sum = wave_add(sum);
@@ -346,28 +440,35 @@ __global__ __launch_bounds__(256) void sample_walk_kernel(SampleParams p, Worksp
 
 template <bool BF16>
 __global__ __launch_bounds__(256) void sample_pick_kernel(SampleParams p, Workspace ws) {
+  __shared__ int s_par[kMaxSlots], s_tok[kMaxSlots];
   __shared__ u64 s_bits[kPart / 64];
-  __shared__ double s_end[256];
-  __shared__ double s_before;
+  __shared__ double s_sum[4], s_left;
   __shared__ int s_part, s_found, s_last;
-  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
-  const int n = p.n_nodes[b];
-  if (n < 1 || n > p.R) return;
-  const Pending pend = ws.pend[b];
-  if (pend.node < 0) return;
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const size_t row0 = (size_t)b * p.R;
   const int parts = sum_parts(p.V);
   const double *sums = ws.part + (size_t)b * parts;
+  // every load that needs no other first
+  const int n = p.n_nodes[b];
+  const Pending pend = ws.pend[b];
+  const double temp = p.temperature[b];
+  const double mine = lane < parts ? sums[lane] : 0.0;
+  if (tid < p.R) {
+    s_par[tid] = tid ? p.parent[row0 + tid] : -1;
+    s_tok[tid] = p.token[row0 + tid];
+  }
+  if (n < 1 || n > p.R || pend.node < 0) return;
   // where the random number falls among the parts: the first whose running sum exceeds it, else
   // the last with any weight
-  if (tid < 64) {
-    double total = 0.0;
-    for (int i = lane; i < parts; i += 64) total += sums[i];
+  if (wave == 0) {
+    double total = mine;
+    for (int i = lane + 64; i < parts; i += 64) total += sums[i];
     total = wave_add(total);
-    const double at = fmax(0.0, pend.u * (total + pend.children) - pend.children);
+    const double at = fmax(0.0, pend.u * (total + pend.kept) - pend.kept);
     double run = 0.0, before = 0.0;
     int found = -1, last = -1;
     for (int i0 = 0; i0 < parts && found < 0; i0 += 64) {
-      const double x = i0 + lane < parts ? sums[i0 + lane] : 0.0;
+      const double x = i0 == 0 ? mine : i0 + lane < parts ? sums[i0 + lane] : 0.0;
       double end = x;
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
@@ -387,7 +488,7 @@ __global__ __launch_bounds__(256) void sample_pick_kernel(SampleParams p, Worksp
     }
     if (lane == 0) {
       s_part = found >= 0 ? found : last;
-      s_before = found >= 0 ? at - before : __builtin_inf();  // what is left within the part
+      s_left = found >= 0 ? at - before : __builtin_inf();  // what is left within the part
       s_found = 0x7fffffff;
       s_last = -1;
     }
@@ -399,9 +500,8 @@ __global__ __launch_bounds__(256) void sample_pick_kernel(SampleParams p, Worksp
     // last of them that has any is the token the random number stands for.
     if (tid == 0)
       for (int t = n - 1; t >= 1; --t) {
-        const int x = p.token[(size_t)b * p.R + t];
-        if (p.parent[(size_t)b * p.R + t] == pend.node && x >= 0 && x < p.V &&
-            logit<BF16>(p.logits, ((size_t)b * p.R + pend.node) * p.V + x) > kNegInf) {
+        const int x = s_tok[t];
+        if (s_par[t] == pend.node && x >= 0 && x < p.V && logit<BF16>(p.logits, (row0 + pend.node) * p.V + x) > kNegInf) {
           p.acc_tok[out] = x;
           break;
         }
@@ -409,31 +509,33 @@ __global__ __launch_bounds__(256) void sample_pick_kernel(SampleParams p, Worksp
     return;
   }
   const int first = s_part * kPart;
-  mark_children(p, b, pend.kids ? n : 0, pend.node, first, s_bits, tid, 256);
+  mark_children(s_par, s_tok, pend.kids ? n : 0, pend.node, first, s_bits, tid);
   double w[16], sum = 0.0;
-  weights16<BF16>(p, (size_t)b * p.R + pend.node, first, s_bits, pend.top, (double)p.temperature[b], tid, w);
+  weights16<BF16>(p, row0 + pend.node, first, s_bits, pend.top, 1.0 / temp, tid, w);
 #pragma unroll
   for (int i = 0; i < 16; ++i) sum += w[i];
-  s_end[tid] = sum;
-  __syncthreads();
+  double end = sum;
 #pragma unroll
-  for (int o = 1; o < 256; o <<= 1) {
-    const double y = tid >= o ? s_end[tid - o] : 0.0;
-    __syncthreads();
-    s_end[tid] += y;
-    __syncthreads();
+  for (int o = 1; o < 64; o <<= 1) {
+    const double y = __shfl_up(end, o);
+    if (lane >= o) end += y;
   }
-  double run = s_end[tid] - sum;
-  const double at = s_before;
+  if (lane == 63) s_sum[wave] = end;
+  __syncthreads();
+  double run = end - sum;
+  for (int i = 0; i < wave; ++i) run += s_sum[i];
+  int found = 0x7fffffff, last = -1;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     run += w[i];
+    const int x = first + 16 * tid + i;
     if (w[i] > 0.0) {
-      const int x = first + 16 * tid + i;
-      if (run > at) atomicMin(&s_found, x);
-      atomicMax(&s_last, x);
+      if (run > s_left) found = min(found, x);
+      last = x;
     }
   }
+  if (found != 0x7fffffff) atomicMin(&s_found, found);
+  if (last >= 0) atomicMax(&s_last, last);
   __syncthreads();
   if (tid == 0) p.acc_tok[out] = s_found != 0x7fffffff ? s_found : s_last;
 }
@@ -441,7 +543,7 @@ __global__ __launch_bounds__(256) void sample_pick_kernel(SampleParams p, Worksp
 template <bool BF16>
 hipError_t launch(const SampleParams &p, hipStream_t stream) {
   const Workspace ws = carve(p.ws, p.B, p.R, p.V);
-  hipLaunchKernelGGL((sample_stats_kernel<BF16>), dim3((unsigned)(p.B * p.R * stat_chunks(p.V))), dim3(256), 0, stream, p, ws);
+  hipLaunchKernelGGL((sample_stats_kernel<BF16>), dim3((unsigned)(p.B * p.R * stat_chunks(p.B * p.R, p.V))), dim3(256), 0, stream, p, ws);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   hipLaunchKernelGGL((sample_walk_kernel<BF16>), dim3((unsigned)(p.B * sum_parts(p.V))), dim3(256), 0, stream, p, ws);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
@@ -452,12 +554,12 @@ hipError_t launch(const SampleParams &p, hipStream_t stream) {
 }  // namespace
 
 size_t accept_sample_workspace(int B, int R, int V) {
-  return round16((size_t)B * R * stat_chunks(V) * sizeof(Stat)) + round16((size_t)B * sum_parts(V) * sizeof(double)) +
+  return round16((size_t)B * R * stat_chunks((long long)B * R, V) * sizeof(Stat)) + round16((size_t)B * sum_parts(V) * sizeof(double)) +
          round16((size_t)B * sizeof(Pending));
 }
 
 bool sample_fits(int B, int R, int V) {
-  return (long long)B * R * stat_chunks(V) < 0x7fffffffLL && (long long)B * sum_parts(V) < 0x7fffffffLL;
+  return (long long)B * R * stat_chunks((long long)B * R, V) < 0x7fffffffLL && (long long)B * sum_parts(V) < 0x7fffffffLL;
 }
 
 hipError_t launch_accept_sample(const SampleParams &p, hipStream_t stream) {
