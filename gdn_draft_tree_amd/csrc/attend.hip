@@ -4,24 +4,37 @@
 // For a request with ctx committed positions and n new rows at positions ctx + t, query row
 // (t, head) attends to every position p < ctx and to the new positions its mask leaves:
 //     o = sum_p w_p v_p / sum_p w_p,   w_p = exp2(c q.k_p - m),   c = scale log2(e),
-// with a running maximum m: one pass over the keys.  Splitting the positions gives partial
+// with a running maximum m: one pass over the keys.  Parts of the positions give partial
 // (m, sum w, sum w v) triples that join by rescaling with exp2(m_i - max m).
 //
 // All G query heads of a key-value head and all rows share its keys, so their R G query rows are
-// the columns of 16-wide MFMA tiles.  Both products take their operands as the cache holds them,
-// straight from global memory to registers, with no LDS between:
-//  * scores, transposed: S^T (keys x queries) = K Q^T on 16x16x32 products.  Lane (g, c) of an
-//    operand holds 8 consecutive channels of one key: a 16-byte load.  The keys of a 32-key tile
-//    go to its two 16-row products in such an order (row r of product h holds key
-//    8 (r / 4) + 4 h + r % 4) that a lane ends up with the scores of the 8 consecutive keys
-//    8 g .. 8 g + 7 of query c;
+// the columns of 16-wide MFMA tiles, and both products take the keys and values as operands of
+// 16x16x32 products:
+//  * scores, transposed: S^T (keys x queries) = K Q^T.  Lane (g, c) of an operand holds 8
+//    consecutive channels of one key.  The keys of a 32-key step go to its two 16-row products in
+//    such an order (row r of product h holds key 8 (r / 4) + 4 h + r % 4) that a lane ends up with
+//    the scores of the 8 consecutive keys 8 g .. 8 g + 7 of query c,
 //  * which is the operand layout the second product needs: O^T (channels x queries) = V^T P^T over
-//    the 32 keys.  Lane (g, c) loads, for each of its keys 8 g + e, the d / 16 consecutive channels
-//    that start at c d / 16 (whole rows, coalesced), and interleaves the keys' 16-bit halves in
-//    registers (v_perm), so that product j has channel c d / 16 + j.
+//    the 32 keys.  Product j has channel c d / 16 + j in row c: a lane reads, for each of its keys,
+//    consecutive channels (whole rows, coalesced), and interleaves the keys' 16-bit halves in
+//    registers (v_perm).
 // The softmax is thus per lane except for the maximum, and that is only joined across lanes when a
 // score exceeds the running one by 2^8: until then the old maximum serves (weights up to 2^8 in
 // fp32 and bf16 lose nothing).
+//
+// Two kernels, by the number of query rows a key-value head has:
+//  * at most 16 (a new token of up to 16 heads a group): the cache's bytes are all there is.
+//    attend_stream_kernel: every wave takes 32-key steps of its own, straight from global memory
+//    to operand registers, no LDS and no barrier until the waves join at the end.
+//  * more (trees, chains): attend_tile_kernel: the four waves of a workgroup have up to two 16-row
+//    tiles each and share 64-key tiles of keys and values, which all of them stage in LDS in
+//    operand order (values already transposed, e4m3 already bf16), one tile ahead.
+//
+// Work is cut by steps, not by requests: the steps of all (key-value head, request) pairs form one
+// list, and each of W workgroups (as many as are resident at once) takes an equal, contiguous part
+// of it, whatever the lengths are; the pairs that a cut goes through leave partial results for
+// attend_join_kernel.  The cuts follow from the lengths on the device, so a captured launch serves
+// any lengths.
 //
 // Arithmetic.  bf16 rows: the products of bf16 numbers are exact, accumulated in fp32; the weights
 // are rounded to bf16 for the second product (half a step, 2^-9 of a weight, against an output
@@ -34,17 +47,15 @@
 namespace gdntree {
 namespace {
 
-constexpr int kTile = 32;         // keys per step of a wave
-constexpr int kWaves = 4;
-constexpr int kItems = 1024;      // workgroups to fill the chip with: 256 CUs, four each
+constexpr int kCUs = 256;
 constexpr float kLazy = 8.f;      // how far (log2) a score may exceed the running maximum
+constexpr float kNegInf = -__builtin_inff();
+constexpr int kMaxPos = 1 << 28;  // positions per request
 
 typedef unsigned long long u64;
 
-__device__ __forceinline__ bf16x8 as_bf16x8(u32x4 x) { return __builtin_bit_cast(bf16x8, x); }
-
-__device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+__device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
 __device__ __forceinline__ unsigned pack_bf16(float lo, float hi) {
@@ -52,37 +63,33 @@ __device__ __forceinline__ unsigned pack_bf16(float lo, float hi) {
   return __builtin_bit_cast(unsigned, r);
 }
 
+// Two e4m3 codes (the low or the high half of w) times a power of two, as bf16.
+template <bool HIGH>
+__device__ __forceinline__ unsigned fp8_pair(unsigned w, float s) {
+  return __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, HIGH));
+}
+
 // Three bf16 parts of eight fp32 numbers, each hi + mid + lo exactly (24 bits); a number that is
 // not finite stays in the high part alone.
-__device__ __forceinline__ void split3(const float x[8], bf16x8 part[3]) {
+__device__ __forceinline__ void split3(const float x[8], u32x4 part[3]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const __bf16 hi = (__bf16)x[i];
-    float r = x[i] - (float)hi;
-    if (!((__float_as_uint((float)hi) & 0x7f800000u) != 0x7f800000u)) r = 0.f;
-    const __bf16 mid = (__bf16)r;
-    part[0][i] = hi;
-    part[1][i] = mid;
-    part[2][i] = (__bf16)(r - (float)mid);
+  for (int k = 0; k < 4; ++k) {
+    const unsigned hi = pack_bf16(x[2 * k], x[2 * k + 1]);
+    const float h0 = __uint_as_float(hi << 16), h1 = __uint_as_float(hi & 0xffff0000u);
+    const float r0 = (hi & 0x7f80u) == 0x7f80u ? 0.f : x[2 * k] - h0;
+    const float r1 = (hi & 0x7f800000u) == 0x7f800000u ? 0.f : x[2 * k + 1] - h1;
+    const unsigned mid = pack_bf16(r0, r1);
+    part[0][k] = hi;
+    part[1][k] = mid;
+    part[2][k] = pack_bf16(r0 - __uint_as_float(mid << 16), r1 - __uint_as_float(mid & 0xffff0000u));
   }
 }
 
-// How the positions of all requests are cut into work items.  Request b has tiles(b) 32-key tiles;
-// an item is at most `span` of them, and the span is the least multiple of the workgroup's waves
-// with which the whole batch makes about kItems workgroups.  It follows from the lengths on the
-// device, so that a captured launch serves any lengths, and is computed by every wave for itself:
-// lane l reads requests l, l + 64, ...
-struct Item {
-  int b;             // request; -1: no item
-  int split, count;  // this item among the request's
-  int slot;          // the request's first partial-result slot (requests of one item have none)
-  int span;          // tiles per item
-};
+// ---- how the work is cut -------------------------------------------------------------------------
 
 struct Lens {
   int ctx, n;  // committed positions, new rows in use (0: no output)
   bool bad;    // positions out of the table's range: the rows in use get NaN
-  int tiles;
 };
 
 __device__ __forceinline__ Lens lens_of(const AttendParams &p, int b) {
@@ -90,93 +97,257 @@ __device__ __forceinline__ Lens lens_of(const AttendParams &p, int b) {
   r.ctx = p.ctx[b];
   r.n = p.n_rows ? p.n_rows[b] : p.R;
   if (r.n < 1 || r.n > p.R) r.n = 0;
-  r.bad = r.ctx < 0 || r.ctx > 0x7fffff00 || (long long)r.ctx + r.n > (long long)p.c.max_pages << p.c.shift;
-  r.tiles = r.n == 0 ? 0 : r.bad ? 1 : (int)(((long long)r.ctx + r.n + kTile - 1) / kTile);
+  r.bad = r.ctx < 0 || r.ctx > kMaxPos - kMaxSlots || r.ctx + r.n > (long long)p.c.max_pages << p.c.shift;
   return r;
 }
 
-__device__ __forceinline__ int wave_scan(int x, int lane) {
+// Steps of `keys` positions of request b (none past the batch's end, or for a request without rows).
+__device__ __forceinline__ int steps_of(const AttendParams &p, int b, int keys) {
+  if (b >= p.B) return 0;
+  const Lens l = lens_of(p, b);
+  return l.n == 0 ? 0 : l.bad ? 1 : (l.ctx + l.n + keys - 1) / keys;
+}
+
+// How the list of steps, ordered by (key-value head, request, step), is cut: W workgroups take equal
+// parts of it, and every row block of BM query rows has a cut of its own (the same one).
+struct Cut {
+  int BM, blocks, W, keys, least;
+};
+
+struct Seg {
+  int h, b;        // b -1: past the end of the list
+  int off, steps;  // the place within the (head, request) pair, and the pair's steps
+};
+
+// A number every lane has, as a scalar.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// Steps of all requests for one head, found by one wave (lane l reads requests l, l + 64, ...).
+__device__ __forceinline__ long long head_steps(const AttendParams &p, int keys, int lane) {
+  long long total = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 64) {
+    int t = steps_of(p, b0 + lane, keys);  // < 2^23 each
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int y = __shfl_up(x, o);
-    if (lane >= o) x += y;
+    for (int o = 32; o > 0; o >>= 1) t += __shfl_xor(t, o);
+    total += uniform(t);
   }
+  return total;
+}
+
+// The place x of the list; per: head_steps.
+__device__ __forceinline__ Seg locate(const AttendParams &p, int keys, long long per, long long x, int lane) {
+  if (x >= per * p.c.H) return Seg{0, -1, 0, 0};
+  const int h = (int)(x / per);
+  long long r = x - h * per;
+  for (int b0 = 0; b0 < p.B; b0 += 64) {
+    const int steps = steps_of(p, b0 + lane, keys);
+    int end = steps;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int y = __shfl_up(end, o);
+      if (lane >= o) end += y;
+    }
+    const u64 mine = __ballot(r >= end - steps && r < end);
+    if (mine) {
+      const int l = uniform(__ffsll((long long)mine) - 1);
+      return Seg{h, b0 + l, (int)r - __builtin_amdgcn_readlane(end - steps, l), __builtin_amdgcn_readlane(steps, l)};
+    }
+    r -= __builtin_amdgcn_readlane(end, 63);
+  }
+  return Seg{0, -1, 0, 0};
+}
+
+// Steps per workgroup: an equal share, and enough that a partial result is worth its join.
+__device__ __forceinline__ long long share_of(long long total, Cut cut) {
+  const long long s = (total + cut.W - 1) / cut.W;
+  return s < cut.least ? cut.least : s;
+}
+
+// A workgroup's part of the list, or (whole: contexts short by the table's width) one pair, with
+// nothing to join.  Workgroups of one part and different row blocks read the same keys: they get
+// ids that differ by 8, so that they follow each other on one XCD and share its L2.
+struct Walk {
+  long long x, end, per;
+  int w, rb;
+  __device__ __forceinline__ Walk(const AttendParams &p, Cut cut, int lane) : x(0), end(1), per(0) {
+    const int id = blockIdx.x, round = 8 * cut.blocks;
+    rb = id % round / 8;
+    w = id / round * 8 + id % 8;
+    if (p.whole) {
+      end = w < p.B * p.c.H;
+    } else {
+      per = head_steps(p, cut.keys, lane);
+      const long long total = per * p.c.H, share = share_of(total, cut);
+      x = w < cut.W ? w * share : total;
+      end = min(total, x + share);
+    }
+  }
+  // The next pair and its steps [t0, t1); false at the end.
+  __device__ __forceinline__ bool next(const AttendParams &p, Cut cut, int lane, Seg &sg, int &t0, int &t1) {
+    if (x >= end) return false;
+    if (p.whole) {
+      sg = Seg{w % p.c.H, w / p.c.H, 0, 0};
+      sg.steps = steps_of(p, sg.b, cut.keys);
+      x = end;
+    } else {
+      sg = locate(p, cut.keys, per, x, lane);
+      if (sg.b < 0) return false;
+    }
+    t0 = sg.off;
+    t1 = p.whole ? sg.steps : (int)min((long long)sg.steps, sg.off + (end - x));
+    x += t1 - t0;
+    return t1 > t0;
+  }
+};
+
+// Where partial results lie: two slots of BM rows per part and row block (the pair a part begins in,
+// and the one it ends in), each row's d sums, and its maximum and sum of weights apart.
+template <int D>
+struct Part {
+  float *base;
+  Cut cut;
+  __device__ __forceinline__ size_t slot(int rb, int w, bool ends) const { return 2 * ((size_t)rb * cut.W + w) + ends; }
+  __device__ __forceinline__ float *sums(size_t slot, int row) const { return base + (slot * cut.BM + row) * D; }
+  __device__ __forceinline__ float *stat(size_t slot, int row) const {
+    return base + (size_t)2 * cut.blocks * cut.W * cut.BM * D + (slot * cut.BM + row) * 2;
+  }
+};
+
+// ---- pieces of both kernels ----------------------------------------------------------------------
+
+// The query rows of a wave's columns as operands (rows not in use are zero) and what they see.
+template <int D, bool BF16ROWS, int MT>
+struct Queries {
+  static constexpr int KS = D / 32, NQ = BF16ROWS ? 1 : 3;
+  u32x4 f[MT][KS][NQ];
+  u64 see[MT];  // bit s - 1: new row s is visible to the column
+
+  // first: query row of column 0 of tile 0; PAIRED: channels as 16-byte loads of 8-bit rows give
+  // them to a lane, else 8 consecutive ones per step
+  template <bool PAIRED>
+  __device__ __forceinline__ void load(const AttendParams &p, const Lens &len, int b, int h, int first, int g, int c) {
+    const int Hq = p.c.H * p.G;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const int m = first + 16 * mt + c, t = m / p.G;
+      const bool used = t < len.n;
+      const size_t row = ((size_t)b * p.R + (used ? t : 0)) * Hq + (size_t)h * p.G + (used ? m % p.G : 0);
+      see[mt] = !used ? 0 : p.anc ? p.anc[(size_t)b * p.R + t] : t >= 64 ? ~0ull : (1ull << t) - 1;
+      if (len.n < 65) see[mt] &= (1ull << (len.n - 1)) - 1;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const int d0 = PAIRED ? 64 * (ks >> 1) + 16 * g + 8 * (ks & 1) : 32 * ks + 8 * g;
+        if constexpr (BF16ROWS) {
+          u32x4 x = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(p.q) + row * D + d0);
+          if (!used) x = u32x4{0, 0, 0, 0};
+          f[mt][ks][0] = x;
+        } else {
+          const float *src = static_cast<const float *>(p.q) + row * D + d0;
+          const f32x4 x0 = *reinterpret_cast<const f32x4 *>(src), x1 = *reinterpret_cast<const f32x4 *>(src + 4);
+          float x[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) { x[i] = used ? x0[i] : 0.f; x[4 + i] = used ? x1[i] : 0.f; }
+          split3(x, f[mt][ks]);
+        }
+      }
+    }
+  }
+};
+
+// Running softmax of one 16-query tile: this lane's column, joined over its four lane groups in m
+// only (l is the lane's own until the end).
+template <int DV>
+struct Running {
+  float m, l;
+  f32x4 acc[DV];
+  __device__ __forceinline__ void clear() {
+    m = kNegInf;
+    l = 0.f;
+#pragma unroll
+    for (int d = 0; d < DV; ++d) acc[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  // The largest of 8 scores (already masked), in the exponent's units.
+  static __device__ __forceinline__ float top_of(const f32x4 s[2], float c) {
+    return c * fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
+                     fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
+  }
+  // Moves the maximum up to at least top, over the column's four lane groups.
+  __device__ __forceinline__ void raise(float top) {
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    const float next = fmaxf(m, top);
+    const float f = m == next ? 1.f : __builtin_amdgcn_exp2f(m - next);
+    m = next;
+    l *= f;
+#pragma unroll
+    for (int d = 0; d < DV; ++d) acc[d] *= f;
+  }
+  __device__ __forceinline__ void weights(const f32x4 s[2], float c, float w[8]) {
+    const float ms = m == kNegInf ? 0.f : m;  // a column that sees nothing yet
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e >> 2][e & 3], c, -ms));
+    l += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+  }
+};
+
+// The scores of the 8 keys from slot s0 (position minus ctx) on, without those a column does not see
+// (see holds no slot past the last one).
+__device__ __forceinline__ void mask_scores(f32x4 s[2], u64 see, int s0) {
+  const int below = min(max(-s0, 0), 8);  // committed positions among them
+  const unsigned near = (((unsigned)see << 1 | 1u) << below) | ((1u << below) - 1u);
+  const unsigned vis = s0 <= 0 ? near : s0 <= 64 ? (unsigned)(see >> (s0 - 1)) : 0u;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s[e >> 2][e & 3] = vis >> e & 1 ? s[e >> 2][e & 3] : kNegInf;
+}
+
+template <bool BF16ROWS>
+__device__ __forceinline__ void weight_operand(const float w[8], u32x4 *pf) {
+  if constexpr (BF16ROWS)
+    pf[0] = u32x4{pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]), pack_bf16(w[4], w[5]), pack_bf16(w[6], w[7])};
+  else
+    split3(w, pf);
+}
+
+__device__ __forceinline__ bool odd_bf16_pair(unsigned x) {
+  return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
+}
+
+// Two bf16 values without those that are not finite.
+__device__ __forceinline__ unsigned clean_pair(unsigned x) {
+  if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
+  if ((x & 0x7f800000u) == 0x7f800000u) x &= 0xffffu;
   return x;
 }
 
-__device__ __forceinline__ int span_of(long long tiles, int units) {
-  const long long least = (tiles * units + kItems - 1) / kItems;
-  return (int)((least + kWaves - 1) / kWaves * kWaves);
-}
-
-// Item j of the batch (the same for every unit of `units` key-value heads and row blocks).
-__device__ __forceinline__ Item find_item(const AttendParams &p, int j, int units, int lane) {
-  long long total = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 64) {
-    long long t = b0 + lane < p.B ? lens_of(p, b0 + lane).tiles : 0;
+// A value that is not finite must not meet a column that does not see it (its weight there is 0,
+// and 0 * inf is NaN), so in the steps that hold new rows such values are left out of the products
+// (clean_pair).  Here, once and rarely, they are added to the columns that do see them: positions
+// [from, to) of the request, sums of channels DV (4 g + i) + d.
+template <int D, bool FP8, int MT>
+__device__ __forceinline__ void add_odd(const AttendParams &p, const Lens &len, const int32_t *tab, int h, int from,
+                                        int to, const u64 (&see)[MT], Running<D / 16> (&run)[MT], int g) {
+  constexpr int DV = D / 16;
+#pragma unroll 1
+  for (int pos = from; pos < to; ++pos) {
+    int page = tab[pos >> p.c.shift];
+    if ((unsigned)page >= (unsigned)p.c.pages) page = 0;  // the result is NaN already
+    const size_t row = p.c.row(page, h, pos);
+    const int sl = pos - len.ctx;
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) t += __shfl_xor(t, o);
-    total += t;
-  }
-  Item it{-1, 0, 0, 0, span_of(total, units)};
-  if (it.span == 0) return it;  // no request has rows
-  int items = 0, slots = 0;     // of the requests before b0
-  for (int b0 = 0; b0 < p.B; b0 += 64) {
-    const int tiles = b0 + lane < p.B ? lens_of(p, b0 + lane).tiles : 0;
-    const int cnt = (tiles + it.span - 1) / it.span, multi = cnt > 1 ? cnt : 0;
-    const int end = wave_scan(cnt, lane), send = wave_scan(multi, lane);
-    const u64 mine = __ballot(j >= items + end - cnt && j < items + end);
-    if (mine) {
-      const int l = __ffsll((long long)mine) - 1;
-      it.b = b0 + l;
-      it.count = __shfl(cnt, l);
-      it.split = j - (items + __shfl(end - cnt, l));
-      it.slot = slots + __shfl(send - multi, l);
-      return it;
-    }
-    items += __shfl(end, 63);
-    slots += __shfl(send, 63);
-  }
-  return it;
-}
-
-// Request b's items (for the join).
-__device__ __forceinline__ Item find_request(const AttendParams &p, int b, int units, int lane) {
-  long long total = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 64) {
-    long long t = b0 + lane < p.B ? lens_of(p, b0 + lane).tiles : 0;
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) t += __shfl_xor(t, o);
-    total += t;
+      for (int d = 0; d < DV; ++d) {
+        const size_t at = row * D + DV * (4 * g + i) + d;
+        float v = 0.f;  // e4m3 has no infinities, and its scales are finite
+        if constexpr (FP8) v = (p.c.v[at] & 0x7fu) == 0x7fu ? __builtin_nanf("") : 0.f;
+        else v = bf16_bits_to_f32(reinterpret_cast<const uint16_t *>(p.c.v)[at]);
+        if ((__float_as_uint(v) & 0x7f800000u) == 0x7f800000u)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+            if (sl <= 0 || (see[mt] >> (sl - 1)) & 1) run[mt].acc[d][i] += v;
+      }
   }
-  Item it{b, 0, 0, 0, span_of(total, units)};
-  if (it.span == 0) return it;
-  for (int b0 = 0; b0 <= b; b0 += 64) {
-    const int tiles = b0 + lane < p.B ? lens_of(p, b0 + lane).tiles : 0;
-    const int cnt = (tiles + it.span - 1) / it.span, multi = cnt > 1 ? cnt : 0;
-    const int send = wave_scan(multi, lane);
-    if (b < b0 + 64) {
-      it.count = __shfl(cnt, b - b0);
-      it.slot += __shfl(send - multi, b - b0);
-    } else {
-      it.slot += __shfl(send, 63);
-    }
-  }
-  return it;
 }
-
-// Upper bounds that hold for any lengths: sum ceil(tiles / span) <= sum tiles / span + B, and a
-// request of two items or more has fewer than twice its tiles / span.
-__host__ __device__ constexpr int items_most(int B, int units) { return (kItems + units - 1) / units + B; }
-__host__ __device__ constexpr int slots_most(int units) { return 2 * ((kItems + units - 1) / units); }
-
-// Partial results: [row block][key-value head][slot][BM][D + 2], the last two (m, sum of weights).
-struct Part {
-  int BM, stride;
-  __device__ __forceinline__ size_t at(int rb, int h, int H, int units, int slot) const {
-    return (((size_t)rb * H + h) * slots_most(units) + slot) * (size_t)BM * stride;
-  }
-};
 
 template <bool BF16>
 __device__ __forceinline__ void store_o(void *o, size_t e, float x) {
@@ -184,172 +355,123 @@ __device__ __forceinline__ void store_o(void *o, size_t e, float x) {
   else static_cast<float *>(o)[e] = x;
 }
 
-// One item: keys [32 t0, 32 t1) of request b for one key-value head and 16 MT query rows.  The
-// waves take every kWaves-th tile each, with statistics and sums of their own, and join in LDS.
-template <int D, bool FP8, bool BF16ROWS, int MT>
-__global__ __launch_bounds__(64 * kWaves, MT == 1 ? 2 : 1) void attend_kernel(AttendParams p) {
+// ---- at most 16 query rows per key-value head ----------------------------------------------------
+
+constexpr int kWaves = 4;
+constexpr int kStreamKeys = 32;
+constexpr int kStreamLeast = 8;  // steps per workgroup: two per wave
+
+// Workgroups resident per CU (by registers): the width of the cut.
+template <int D, bool BF16ROWS>
+constexpr int stream_groups() { return D == 64 ? 4 : BF16ROWS ? 3 : 2; }
+
+template <int D, bool FP8, bool BF16ROWS>
+__global__ __launch_bounds__(64 * kWaves, (stream_groups<D, BF16ROWS>())) void attend_stream_kernel(AttendParams p) {
   constexpr int KS = D / 32;               // 32-channel steps of the scores' product
   constexpr int DV = D / 16;               // channels per lane of the values' product
   constexpr int NQ = BF16ROWS ? 1 : 3;     // bf16 parts of q and of the weights
-  constexpr int BM = 16 * MT;
+  constexpr int BM = 16;
   constexpr int OST = D + 4;               // padded row of the joined sums
   __shared__ float s_o[BM * OST];
   __shared__ float s_m[kWaves][BM], s_l[kWaves][BM];
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int c = lane & 15, g = lane >> 4;
-  const int rows = p.R * p.G;              // query rows of a key-value head
-  const int nrb = (rows + BM - 1) / BM, units = nrb * p.c.H;
-  const int rb = blockIdx.x % nrb, h = blockIdx.x / nrb % p.c.H, j = blockIdx.x / units;
-  const Item it = find_item(p, j, units, lane);
-  if (it.b < 0) return;
-  const int b = it.b;
-  const Lens len = lens_of(p, b);
-  if (rb * BM >= len.n * p.G) return;      // no row of this block is in use
-  const int Hq = p.c.H * p.G;
-  const int total = len.ctx + len.n;
+  constexpr Cut cut{BM, 1, kCUs * stream_groups<D, BF16ROWS>(), kStreamKeys, kStreamLeast};
+  const Part<D> part{p.part, cut};
+  Walk walk(p, cut, lane);
+  Seg sg;
+  int t0, t1;
+  while (walk.next(p, cut, lane, sg, t0, t1)) {
+    const int b = sg.b, h = sg.h;
+    const Lens len = lens_of(p, b);
+    const int Hq = p.c.H * p.G, total = len.ctx + len.n;
+    Queries<D, BF16ROWS, 1> q;
+    q.template load<FP8>(p, len, b, h, 0, g, c);
+    Running<DV> run[1];
+    run[0].clear();
+    bool odd = false;                        // a new row's value is not finite
+    const int32_t *tab = p.c.table + (size_t)b * p.c.max_pages;
+    bool bad = len.bad;                      // or a page id out of range
 
-  // the query rows of this lane's columns, as operands; rows not in use are zero
-  bf16x8 qf[MT][KS][NQ];
-  u64 see[MT];                             // bit s - 1: new row s is visible to the column
+    // Positions past the last row are loaded as the last row (and masked), pages out of range as page 0
+    // (and the result becomes NaN): every load is in bounds.  The page ids are loaded a step ahead.
+    int next_k = 0, next_v = 0;
+    const auto ids = [&](int t) {
+      next_k = tab[min(t * kStreamKeys + 8 * (c >> 2), total - 1) >> p.c.shift];
+      next_v = tab[min(t * kStreamKeys + 8 * g, total - 1) >> p.c.shift];
+    };
+    if (t0 + wave < t1 && !len.bad) ids(t0 + wave);
+    for (int t = t0 + wave; t < t1 && !len.bad; t += kWaves) {
+      const int pos0 = t * kStreamKeys;
+      const int pk = min(pos0 + 8 * (c >> 2), total - 1), pv = min(pos0 + 8 * g, total - 1);
+      int pgk = next_k, pgv = next_v;
+      if ((unsigned)pgk >= (unsigned)p.c.pages) { bad = true; pgk = 0; }
+      if ((unsigned)pgv >= (unsigned)p.c.pages) { bad = true; pgv = 0; }
+
+      u32x4 kr[2][KS];                       // bf16 operands of the two 16-key products
+      u32x4 vr[8];                           // DV bf16 channels of keys 8 g + e
+      if constexpr (FP8) {
+        const u64 ksc = *reinterpret_cast<const u64 *>(p.c.ks + p.c.row(pgk, h, pk & ~7));
+        const u64 vsc = *reinterpret_cast<const u64 *>(p.c.vs + p.c.row(pgv, h, pv & ~7));
+        u32x4 raw[2][KS / 2];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    const int m = rb * BM + 16 * mt + c, t = m / p.G;
-    const bool used = t < len.n;
-    const size_t qrow = ((size_t)b * p.R + (used ? t : 0)) * Hq + (size_t)h * p.G + (used ? m % p.G : 0);
-    see[mt] = !used ? 0 : p.anc ? p.anc[(size_t)b * p.R + t] : t >= 64 ? ~0ull : (1ull << t) - 1;
-    if (len.n < 65) see[mt] &= (1ull << (len.n - 1)) - 1;
+        for (int hh = 0; hh < 2; ++hh) {
+          const int pos = min(pos0 + 8 * (c >> 2) + 4 * hh + (c & 3), total - 1);
+          const unsigned char *src = p.c.k + p.c.row(pgk, h, pos) * D + 16 * g;
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      // channels of this lane in step ks: as the cache rows' loads give them
-      const int d0 = FP8 ? 64 * (ks >> 1) + 16 * g + 8 * (ks & 1) : 32 * ks + 8 * g;
-      if constexpr (BF16ROWS) {
-        u32x4 x = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(p.q) + qrow * D + d0);
-        if (!used) x = u32x4{0, 0, 0, 0};
-        qf[mt][ks][0] = as_bf16x8(x);
+          for (int s2 = 0; s2 < KS / 2; ++s2) raw[hh][s2] = *reinterpret_cast<const u32x4 *>(src + 64 * s2);
+        }
+        u32x2 vraw[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int pos = min(pos0 + 8 * g + e, total - 1);
+          const unsigned char *src = p.c.v + p.c.row(pgv, h, pos) * D + DV * c;
+          if constexpr (DV == 8) vraw[e] = *reinterpret_cast<const u32x2 *>(src);
+          else vraw[e] = u32x2{*reinterpret_cast<const unsigned *>(src), 0u};
+        }
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const int pos = min(pos0 + 8 * (c >> 2) + 4 * hh + (c & 3), total - 1);
+          const float s = scale_of((unsigned)(ksc >> (8 * (pos & 7))) & 255u);
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const unsigned src = raw[hh][ks >> 1][2 * (ks & 1) + (w >> 1)];
+              kr[hh][ks][w] = w & 1 ? fp8_pair<true>(src, s) : fp8_pair<false>(src, s);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int pos = min(pos0 + 8 * g + e, total - 1);
+          const float s = scale_of((unsigned)(vsc >> (8 * (pos & 7))) & 255u);
+#pragma unroll
+          for (int w = 0; w < DV / 2; ++w) vr[e][w] = w & 1 ? fp8_pair<true>(vraw[e][w >> 1], s) : fp8_pair<false>(vraw[e][w >> 1], s);
+        }
       } else {
-        const float *src = static_cast<const float *>(p.q) + qrow * D + d0;
-        const f32x4 x0 = *reinterpret_cast<const f32x4 *>(src), x1 = *reinterpret_cast<const f32x4 *>(src + 4);
-        float x[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) { x[i] = used ? x0[i] : 0.f; x[4 + i] = used ? x1[i] : 0.f; }
-        split3(x, qf[mt][ks]);
-      }
-    }
-  }
-
-  f32x4 acc[MT][DV];
-  float m_run[MT], l_run[MT];
+        for (int hh = 0; hh < 2; ++hh) {
+          const int pos = min(pos0 + 8 * (c >> 2) + 4 * hh + (c & 3), total - 1);
+          const unsigned char *src = p.c.k + p.c.row(pgk, h, pos) * (2 * D) + 16 * g;
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    m_run[mt] = -__builtin_inff();
-    l_run[mt] = 0.f;
+          for (int ks = 0; ks < KS; ++ks) kr[hh][ks] = *reinterpret_cast<const u32x4 *>(src + 64 * ks);
+        }
 #pragma unroll
-    for (int d = 0; d < DV; ++d) acc[mt][d] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
-
-  const int tiles = len.bad ? 0 : len.tiles;
-  const int t0 = it.split * it.span, t1 = min(tiles, t0 + it.span);
-  const int32_t *tab = p.c.table + (size_t)b * p.c.max_pages;
-  bool bad = false;                        // a page id out of range
-
-  for (int tile = t0 + wave; tile < t1; tile += kWaves) {
-    const int pos0 = tile * kTile;
-    // Positions past the last row are loaded as the last row (and masked), pages out of range as
-    // page 0 (and the result becomes NaN): every load is in bounds.
-    const int pk = min(pos0 + 8 * (c >> 2), total - 1), pv = min(pos0 + 8 * g, total - 1);
-    int pgk = tab[pk >> p.c.shift], pgv = tab[pv >> p.c.shift];
-    if ((unsigned)pgk >= (unsigned)p.c.pages) { bad = true; pgk = 0; }
-    if ((unsigned)pgv >= (unsigned)p.c.pages) { bad = true; pgv = 0; }
-
-    u32x4 kr[2][KS];                       // bf16 operands of the two 16-key products
-    u32x4 vr[8];                           // DV bf16 channels of keys 8 g + e
-    if constexpr (FP8) {
-      const u64 ksc = *reinterpret_cast<const u64 *>(p.c.ks + p.c.row(pgk, h, pk & ~7));
-      const u64 vsc = *reinterpret_cast<const u64 *>(p.c.vs + p.c.row(pgv, h, pv & ~7));
-      u32x4 raw[2][KS / 2];
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const int pos = min(pos0 + 8 * (c >> 2) + 4 * hh + (c & 3), total - 1);
-        const unsigned char *src = p.c.k + p.c.row(pgk, h, pos) * D + 16 * g;
-#pragma unroll
-        for (int s2 = 0; s2 < KS / 2; ++s2) raw[hh][s2] = *reinterpret_cast<const u32x4 *>(src + 64 * s2);
-      }
-      u32x2 vraw[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int pos = min(pos0 + 8 * g + e, total - 1);
-        const unsigned char *src = p.c.v + p.c.row(pgv, h, pos) * D + DV * c;
-        if constexpr (DV == 8) vraw[e] = *reinterpret_cast<const u32x2 *>(src);
-        else vraw[e] = u32x2{*reinterpret_cast<const unsigned *>(src), 0u};
-      }
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const int pos = min(pos0 + 8 * (c >> 2) + 4 * hh + (c & 3), total - 1);
-        const float s = scale_of((unsigned)(ksc >> (8 * (pos & 7))) & 255u);
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const unsigned src = raw[hh][ks >> 1][2 * (ks & 1) + (w >> 1)];
-            kr[hh][ks][w] = __builtin_bit_cast(unsigned, w & 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(src, s, true)
-                                                               : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(src, s, false));
+        for (int e = 0; e < 8; ++e) {
+          const int pos = min(pos0 + 8 * g + e, total - 1);
+          const unsigned char *src = p.c.v + p.c.row(pgv, h, pos) * (2 * D) + 2 * DV * c;
+          if constexpr (DV == 8) {
+            vr[e] = *reinterpret_cast<const u32x4 *>(src);
+          } else {
+            const u32x2 y = *reinterpret_cast<const u32x2 *>(src);
+            vr[e] = u32x4{y[0], y[1], 0u, 0u};
           }
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int pos = min(pos0 + 8 * g + e, total - 1);
-        const float s = scale_of((unsigned)(vsc >> (8 * (pos & 7))) & 255u);
-#pragma unroll
-        for (int w = 0; w < DV / 2; ++w)
-          vr[e][w] = __builtin_bit_cast(unsigned, w & 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(vraw[e][w >> 1], s, true)
-                                                        : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(vraw[e][w >> 1], s, false));
-      }
-    } else {
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const int pos = min(pos0 + 8 * (c >> 2) + 4 * hh + (c & 3), total - 1);
-        const unsigned char *src = p.c.k + p.c.row(pgk, h, pos) * (2 * D) + 16 * g;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) kr[hh][ks] = *reinterpret_cast<const u32x4 *>(src + 64 * ks);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int pos = min(pos0 + 8 * g + e, total - 1);
-        const unsigned char *src = p.c.v + p.c.row(pgv, h, pos) * (2 * D) + 2 * DV * c;
-        if constexpr (DV == 8) {
-          vr[e] = *reinterpret_cast<const u32x4 *>(src);
-        } else {
-          const u32x2 x = *reinterpret_cast<const u32x2 *>(src);
-          vr[e] = u32x4{x[0], x[1], 0u, 0u};
         }
       }
-    }
 
-    const bool masked = pos0 + kTile > len.ctx;  // the tile holds new rows, or ends past the last one
-    // A masked value that is not finite would enter the sums as 0 * inf: such tiles (new rows only)
-    // are summed term by term over what each column sees.
-    bool odd = false;
-    if (masked) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-#pragma unroll
-        for (int w = 0; w < DV / 2; ++w)
-          odd = odd || (vr[e][w] & 0x7f80u) == 0x7f80u || (vr[e][w] & 0x7f800000u) == 0x7f800000u;
-      odd = __any(odd);
-    }
-    bf16x8 vt[DV];  // operand j: channel DV c + j of the 8 keys
-#pragma unroll
-    for (int d = 0; d < DV; ++d) {
-      u32x4 x;
-#pragma unroll
-      for (int w = 0; w < 4; ++w)
-        x[w] = __builtin_amdgcn_perm(vr[2 * w + 1][d >> 1], vr[2 * w][d >> 1], d & 1 ? 0x07060302u : 0x05040100u);
-      vt[d] = as_bf16x8(x);
-    }
-
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+      if (t + kWaves < t1) ids(t + kWaves);
+      const bool masked = pos0 + kStreamKeys > len.ctx;  // the step holds new rows, or ends past the last one
       f32x4 s[2];
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
@@ -357,200 +479,512 @@ __global__ __launch_bounds__(64 * kWaves, MT == 1 ? 2 : 1) void attend_kernel(At
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-          for (int q = NQ - 1; q >= 0; --q) s[hh] = mfma(as_bf16x8(kr[hh][ks]), qf[mt][ks][q], s[hh]);
+          for (int i = NQ - 1; i >= 0; --i) s[hh] = mfma(kr[hh][ks], q.f[0][ks][i], s[hh]);
       }
-      unsigned vis = 0xffu;  // which of the 8 keys the column sees
       if (masked) {
-        vis = 0;
+        mask_scores(s, q.see[0], pos0 + 8 * g - len.ctx);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int sl = pos0 + 8 * g + e - len.ctx;
-          const bool on = sl <= 0 || (sl < len.n && ((see[mt] >> (sl - 1)) & 1));
-          vis |= (unsigned)on << e;
-          if (!on) s[e >> 2][e & 3] = -__builtin_inff();
-        }
-      }
-      float top = s[0][0];
+        for (int e = 0; e < 8; ++e)
 #pragma unroll
-      for (int e = 1; e < 8; ++e) top = fmaxf(top, s[e >> 2][e & 3]);
-      top *= p.scale_log2;
-      if (__any(top > m_run[mt] + kLazy)) {
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float m_new = fmaxf(m_run[mt], top);
-        const float f = m_run[mt] == m_new ? 1.f : __builtin_amdgcn_exp2f(m_run[mt] - m_new);
-        m_run[mt] = m_new;
-        l_run[mt] *= f;
-#pragma unroll
-        for (int d = 0; d < DV; ++d) acc[mt][d] *= f;
-      }
-      const float ms = m_run[mt] == -__builtin_inff() ? 0.f : m_run[mt];  // a column that sees nothing yet
-      float w[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        w[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e >> 2][e & 3], p.scale_log2, -ms));
-        l_run[mt] += w[e];
-      }
-      if (!odd) {
-        bf16x8 pf[NQ];
-        if constexpr (BF16ROWS)
-          pf[0] = as_bf16x8(u32x4{pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]), pack_bf16(w[4], w[5]), pack_bf16(w[6], w[7])});
-        else
-          split3(w, pf);
-#pragma unroll
-        for (int d = 0; d < DV; ++d)
-#pragma unroll
-          for (int q = NQ - 1; q >= 0; --q) acc[mt][d] = mfma(vt[d], pf[q], acc[mt][d]);
-      } else {
-        for (int gk = 0; gk < 4; ++gk) {
-          const unsigned seen = (unsigned)__shfl((int)vis, 16 * gk + c);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float we = __shfl(w[e], 16 * gk + c);
-            const bool on = (seen >> e) & 1;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int d2 = 0; d2 < DV / 2; ++d2) {
-                const unsigned v2 = (unsigned)__shfl((int)vr[e][d2], 16 * gk + 4 * g + i);
-                if (on) {
-                  acc[mt][2 * d2][i] += we * __uint_as_float(v2 << 16);
-                  acc[mt][2 * d2 + 1][i] += we * __uint_as_float(v2 & 0xffff0000u);
-                }
-              }
+          for (int w = 0; w < DV / 2; ++w) {
+            odd = odd || odd_bf16_pair(vr[e][w]);
+            vr[e][w] = clean_pair(vr[e][w]);
           }
-        }
+      }
+      const float top = Running<DV>::top_of(s, p.scale_log2);
+      if (__any(top > run[0].m + kLazy)) run[0].raise(top);
+      float w[8];
+      run[0].weights(s, p.scale_log2, w);
+      u32x4 pf[NQ];
+      weight_operand<BF16ROWS>(w, pf);
+#pragma unroll
+      for (int d = 0; d < DV; ++d) {
+        u32x4 vt;  // channel DV c + d of the 8 keys
+#pragma unroll
+        for (int k2 = 0; k2 < 4; ++k2)
+          vt[k2] = __builtin_amdgcn_perm(vr[2 * k2 + 1][d >> 1], vr[2 * k2][d >> 1], d & 1 ? 0x07060302u : 0x05040100u);
+#pragma unroll
+        for (int i = NQ - 1; i >= 0; --i) run[0].acc[d] = mfma(vt, pf[i], run[0].acc[d]);
       }
     }
-  }
+    if (__any(odd))
+      for (int t = t0 + wave; t < t1; t += kWaves)
+        if ((t + 1) * kStreamKeys > len.ctx)
+          add_odd<D, FP8, 1>(p, len, tab, h, t * kStreamKeys, min((t + 1) * kStreamKeys, total), q.see, run, g);
 
-  // the column's sum of weights over the lane groups, then the waves joined
-  bad = __any(bad) || len.bad;
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    float l = l_run[mt];
+    // the column's sum of weights over the lane groups, then the waves joined
+    float l = run[0].l;
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
-    if (bad) l = __builtin_nanf("");
+    if (__any(bad)) l = __builtin_nanf("");
     if (g == 0) {
-      s_m[wave][16 * mt + c] = m_run[mt];
-      s_l[wave][16 * mt + c] = l;
+      s_m[wave][c] = run[0].m;
+      s_l[wave][c] = l;
     }
-  }
-  __syncthreads();
-  float fac[MT], m_all[MT], l_all[MT];
+    __syncthreads();
+    float m_all = s_m[0][c], l_all = 0.f, mine = 0.f;
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    const int col = 16 * mt + c;
-    float m = s_m[0][col];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) m = fmaxf(m, s_m[w][col]);
-    m_all[mt] = m;
-    l_all[mt] = 0.f;
+    for (int w = 1; w < kWaves; ++w) m_all = fmaxf(m_all, s_m[w][c]);
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-      const float f = s_m[w][col] == m ? 1.f : __builtin_amdgcn_exp2f(s_m[w][col] - m);
-      l_all[mt] += s_l[w][col] * f;
-      if (w == wave) fac[mt] = f;
+      const float f = s_m[w][c] == m_all ? 1.f : __builtin_amdgcn_exp2f(s_m[w][c] - m_all);
+      l_all += s_l[w][c] * f;
+      if (w == wave) mine = f;
     }
-  }
-  for (int w = 0; w < kWaves; ++w) {  // in order: the sums do not depend on which wave is first
-    if (w == wave) {
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+    for (int w = 0; w < kWaves; ++w) {  // in order: the sums do not depend on which wave is first
+      if (w == wave) {
 #pragma unroll
         for (int d = 0; d < DV; ++d)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float *dst = &s_o[(16 * mt + c) * OST + DV * (4 * g + i) + d];
-            const float x = acc[mt][d][i] * fac[mt];
-            *dst = w == 0 ? x : *dst + x;
+            float *dst = &s_o[c * OST + DV * (4 * g + i) + d];
+            const float y = run[0].acc[d][i] * mine;
+            *dst = w == 0 ? y : *dst + y;
           }
+      }
+      __syncthreads();
+    }
+    if (wave == 0 && g == 0) {
+      s_m[0][c] = m_all;
+      s_l[0][c] = l_all;
+    }
+    __syncthreads();
+    const bool whole = t0 == 0 && t1 == sg.steps;
+    const size_t slot = part.slot(0, walk.w, t0 == 0);
+    const int rows = len.n * p.G;
+    for (int e = tid; e < rows * D; e += 64 * kWaves) {
+      const int r = e / D, d = e % D;
+      const float y = s_o[r * OST + d];
+      if (whole)
+        store_o<BF16ROWS>(p.o, (((size_t)b * p.R + r / p.G) * Hq + (size_t)h * p.G + r % p.G) * D + d, y / s_l[0][r]);
+      else
+        part.sums(slot, r)[d] = y;
+    }
+    if (!whole && tid < rows) {
+      part.stat(slot, tid)[0] = s_m[0][tid];
+      part.stat(slot, tid)[1] = s_l[0][tid];
+    }
+    __syncthreads();  // the next triple's sums go to the same place
+  }
+}
+
+// ---- more query rows -----------------------------------------------------------------------------
+
+constexpr int kTileKeys = 64;
+constexpr int kTileLeast = 4;  // tiles per workgroup
+
+// Four waves of up to MT 16-row tiles each, two workgroups a CU: 256 registers, of which a tile's sums
+// take 32 and its queries 16 (48 split), so two tiles fit beside what is in flight (split: one).  (One workgroup a CU with
+// 512 registers and up to six tiles: half of the registers are reachable by the matrix
+// instructions only, and the copies between the halves cost more than the products.)
+constexpr int kTileGroups = 2;
+constexpr int tile_most(bool bf16_rows) { return bf16_rows ? 2 : 1; }
+
+// One workgroup's staging of a 64-key tile: what a thread holds between loading and storing it.
+// each of 256 (d = 128) or 128 threads has eight keys of four value channels, and each of 256 a quarter
+// of one key row (all its 16-byte chunks of one residue mod 4).
+template <int D, bool FP8>
+struct Stage {
+  static constexpr int KS = D / 32, DV = D / 16;
+  static constexpr int VC = D / 4;                       // threads per 8 keys of values
+  static constexpr int JV = 8 * VC;                      // value threads
+  static constexpr int KC = FP8 ? D / 64 : D / 32;       // 16-byte loads per key thread
+  u32x2 v[8];                                            // four channels of eight keys (e4m3: first half)
+  u32x4 k[KC];
+  u64 vsc;
+  unsigned ksc;
+  int pgv, pgk;                                          // page ids of the tile to be loaded next
+  bool has_v;
+  int kg, cc, row, quarter;
+
+  __device__ __forceinline__ void init(int tid) {
+    has_v = tid < JV;
+    kg = (tid / VC) & 7;
+    cc = tid % VC;
+    row = tid >> 2;
+    quarter = tid & 3;
+  }
+  // Positions past the last row are loaded as rows of the last group or as the last row (and masked),
+  // pages out of range as page 0 (and the result becomes NaN): every load is in bounds.  The ids are
+  // loaded a tile before they are looked at, so that nothing waits for them.
+  __device__ __forceinline__ int group(int pos0, int total) const { return min(pos0 + 8 * kg, (total - 1) & ~7); }
+  __device__ __forceinline__ void pages(const AttendParams &p, const int32_t *tab, int pos0, int total) {
+    pgv = tab[group(pos0, total) >> p.c.shift];
+    pgk = tab[min(pos0 + row, total - 1) >> p.c.shift];
+  }
+  __device__ __forceinline__ void load(const AttendParams &p, int h, int pos0, int total, bool &bad) {
+    if ((unsigned)pgv >= (unsigned)p.c.pages) { bad = true; pgv = 0; }
+    if ((unsigned)pgk >= (unsigned)p.c.pages) { bad = true; pgk = 0; }
+    const size_t rk = p.c.row(pgk, h, min(pos0 + row, total - 1));
+    const unsigned char *src = p.c.k + rk * (FP8 ? D : 2 * D) + 16 * quarter;
+#pragma unroll
+    for (int i = 0; i < KC; ++i) k[i] = *reinterpret_cast<const u32x4 *>(src + 64 * i);
+    if constexpr (FP8) ksc = p.c.ks[rk];
+    if (JV == 256 || has_v) {
+      const int at = group(pos0, total);
+      const size_t rv = p.c.row(pgv, h, at);
+      const unsigned char *vs = p.c.v + rv * (FP8 ? D : 2 * D) + (FP8 ? 4 : 8) * cc;
+      const int last = total - 1 - at;
+      const auto one = [&](int e, int from) {
+        if constexpr (FP8) v[e][0] = *reinterpret_cast<const unsigned *>(vs + from * D);
+        else v[e] = *reinterpret_cast<const u32x2 *>(vs + from * (2 * D));
+      };
+      if (pos0 + kTileKeys <= total) {  // constant offsets
+#pragma unroll
+        for (int e = 0; e < 8; ++e) one(e, e);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) one(e, min(e, last));
+      }
+      if constexpr (FP8) vsc = *reinterpret_cast<const u64 *>(p.c.vs + rv);
+    }
+  }
+  // Stores the loaded tile as operands: keys [32-key half][product][channel step][lane], values
+  // [half][product][lane], 16 bytes each.  masked: the tile holds new rows.
+  __device__ __forceinline__ void store(u32x4 *sk, u32x4 *sv, int pos0, int total, bool masked, bool &odd) const {
+    if (JV == 256 || has_v) {
+      u32x2 x[8];
+      const int last = total - 1 - group(pos0, total);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if constexpr (FP8) {
+          const float s = scale_of((unsigned)(vsc >> (8 * min(e, last))) & 255u);
+          x[e] = u32x2{fp8_pair<false>(v[e][0], s), fp8_pair<true>(v[e][0], s)};
+        } else {
+          x[e] = v[e];
+        }
+        if (masked) {
+          odd = odd || odd_bf16_pair(x[e][0]) || odd_bf16_pair(x[e][1]);
+          x[e] = u32x2{clean_pair(x[e][0]), clean_pair(x[e][1])};
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        u32x4 y;
+#pragma unroll
+        for (int k2 = 0; k2 < 4; ++k2)
+          y[k2] = __builtin_amdgcn_perm(x[2 * k2 + 1][j >> 1], x[2 * k2][j >> 1], j & 1 ? 0x07060302u : 0x05040100u);
+        const int ch = 4 * cc + j;
+        sv[((kg >> 2) * DV + ch % DV) * 64 + (kg & 3) * 16 + ch / DV] = y;
+      }
+    }
+    const int at = ((row >> 5) * 2 + ((row >> 2) & 1)) * KS, r = 4 * ((row & 31) >> 3) + (row & 3);
+#pragma unroll
+    for (int i = 0; i < KC; ++i) {
+      if constexpr (FP8) {
+        const float s = scale_of(ksc);
+        const int q = quarter + 4 * i;  // channels 16 q .. 16 q + 15
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+          sk[(at + (q >> 1)) * 64 + (2 * (q & 1) + hf) * 16 + r] =
+              u32x4{fp8_pair<false>(k[i][2 * hf], s), fp8_pair<true>(k[i][2 * hf], s),
+                    fp8_pair<false>(k[i][2 * hf + 1], s), fp8_pair<true>(k[i][2 * hf + 1], s)};
+      } else {
+        sk[(at + i) * 64 + quarter * 16 + r] = k[i];
+      }
+    }
+  }
+};
+
+// One 32-key half of a staged tile for a wave's NT 16-row tiles.
+template <int D, bool BF16ROWS, int NT>
+__device__ __forceinline__ void tile_half(const u32x4 *sk, const u32x4 *sv, const Queries<D, BF16ROWS, NT> &q,
+                                          Running<D / 16> (&run)[NT], float scale_log2, int lane, int slot0) {
+  constexpr int KS = D / 32, DV = D / 16, NQ = BF16ROWS ? 1 : 3;
+  const int g = lane >> 4;
+  f32x4 s[NT][2];
+#pragma unroll
+  for (int mt = 0; mt < NT; ++mt) s[mt][0] = s[mt][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+  u32x4 kf[2 * KS], vf[DV];
+#pragma unroll
+  for (int i = 0; i < 2 * KS; ++i) kf[i] = sk[i * 64 + lane];
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+      for (int mt = 0; mt < NT; ++mt)
+#pragma unroll
+        for (int i = NQ - 1; i >= 0; --i) s[mt][hh] = mfma(kf[hh * KS + ks], q.f[mt][ks][i], s[mt][hh]);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int d = 0; d < DV; ++d) vf[d] = sv[d * 64 + lane];
+  __builtin_amdgcn_sched_barrier(0);
+  if (slot0 + 32 > 0)  // new rows, or positions past the last one
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt) mask_scores(s[mt], q.see[mt], slot0 + 8 * g);
+  float top[NT];
+  bool more = false;
+#pragma unroll
+  for (int mt = 0; mt < NT; ++mt) {
+    top[mt] = Running<DV>::top_of(s[mt], scale_log2);
+    more = more || top[mt] > run[mt].m + kLazy;
+  }
+  if (__any(more))
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt) run[mt].raise(top[mt]);
+  u32x4 pf[NT][NQ];
+#pragma unroll
+  for (int mt = 0; mt < NT; ++mt) {
+    float w[8];
+    run[mt].weights(s[mt], scale_log2, w);
+    weight_operand<BF16ROWS>(w, pf[mt]);
+  }
+#pragma unroll
+  for (int d = 0; d < DV; ++d)
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt)
+#pragma unroll
+      for (int i = NQ - 1; i >= 0; --i) run[mt].acc[d] = mfma(vf[d], pf[mt][i], run[mt].acc[d]);
+}
+
+// Steps [t0, t1) of a pair by a wave with NT 16-row tiles from row tile mt0 of the block on.  Waves of
+// one workgroup may differ in NT: they stage together and meet at the same barriers.
+template <int D, bool FP8, bool BF16ROWS, int NT>
+__device__ __forceinline__ void tile_pair(const AttendParams &p, const Part<D> &part, const Lens &len, Stage<D, FP8> &stage,
+                                          u32x4 *s_k, u32x4 *s_v, int b, int h, int first, int rows, int mt0, int t0,
+                                          int t1, bool whole, size_t slot, int lane) {
+  constexpr int DV = D / 16, KF = 2 * (D / 32) * 64, VF = DV * 64;  // 16-byte pieces of a 32-key half
+  constexpr int N1 = NT > 0 ? NT : 1;
+  const int c = lane & 15, g = lane >> 4, Hq = p.c.H * p.G, total = len.ctx + len.n;
+  Queries<D, BF16ROWS, N1> q;
+  Running<DV> run[N1];
+  if constexpr (NT > 0) {
+    q.template load<false>(p, len, b, h, first + 16 * mt0, g, c);
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt) run[mt].clear();
+  }
+  bool bad = len.bad, odd = false;  // a page id out of range; a new row's value is not finite
+  if (!len.bad) {
+    const int32_t *tab = p.c.table + (size_t)b * p.c.max_pages;
+    stage.pages(p, tab, t0 * kTileKeys, total);
+    stage.load(p, h, t0 * kTileKeys, total, bad);
+    if (t0 + 1 < t1) stage.pages(p, tab, (t0 + 1) * kTileKeys, total);
+    stage.store(s_k, s_v, t0 * kTileKeys, total, (t0 + 1) * kTileKeys > len.ctx, odd);
+    __syncthreads();
+    for (int t = t0; t < t1; ++t) {
+      const int buf = (t - t0) & 1, pos0 = t * kTileKeys;
+      if (t + 1 < t1) {
+        stage.load(p, h, pos0 + kTileKeys, total, bad);
+        if (t + 2 < t1) stage.pages(p, tab, pos0 + 2 * kTileKeys, total);
+      }
+      if constexpr (NT > 0)
+        for (int hf = 0; hf < 2; ++hf)
+          tile_half<D, BF16ROWS, NT>(s_k + (2 * buf + hf) * KF, s_v + (2 * buf + hf) * VF, q, run, p.scale_log2, lane,
+                                     pos0 + 32 * hf - len.ctx);
+      if (t + 1 < t1) {
+        stage.store(s_k + 2 * (buf ^ 1) * KF, s_v + 2 * (buf ^ 1) * VF, pos0 + kTileKeys, total,
+                    pos0 + 2 * kTileKeys > len.ctx, odd);
+        __syncthreads();
+      }
+    }
+    odd = __syncthreads_or(odd);
+    if constexpr (NT > 0)
+      if (odd)
+        add_odd<D, FP8, NT>(p, len, tab, h, max(t0, len.ctx / kTileKeys) * kTileKeys, min(t1 * kTileKeys, total), q.see, run, g);
+  }
+  bad = __syncthreads_or(bad);  // and all waves are done with the last tile
+  if constexpr (NT > 0) {
+#pragma unroll
+    for (int mt = 0; mt < NT; ++mt) {
+      float l = run[mt].l;
+      l += __shfl_xor(l, 16);
+      l += __shfl_xor(l, 32);
+      if (bad) l = __builtin_nanf("");
+      const int r = 16 * (mt0 + mt) + c, m = first + r;
+      if (r >= rows) continue;
+      if (!whole && g == 0) {
+        part.stat(slot, r)[0] = run[mt].m;
+        part.stat(slot, r)[1] = l;
+      }
+      const float inv = 1.f / l;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // channels DV (4 g + i) .. + DV - 1
+        float y[DV];
+#pragma unroll
+        for (int d = 0; d < DV; ++d) y[d] = whole ? run[mt].acc[d][i] * inv : run[mt].acc[d][i];
+        const int ch = DV * (4 * g + i);
+        const size_t at = (((size_t)b * p.R + m / p.G) * Hq + (size_t)h * p.G + m % p.G) * D + ch;
+        if (whole && BF16ROWS) {
+          uint16_t *dst = static_cast<uint16_t *>(p.o) + at;
+          if constexpr (DV == 8)
+            *reinterpret_cast<u32x4 *>(dst) = u32x4{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7])};
+          else
+            *reinterpret_cast<u32x2 *>(dst) = u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+        } else {
+          float *dst = whole ? static_cast<float *>(p.o) + at : part.sums(slot, r) + ch;
+#pragma unroll
+          for (int d = 0; d < DV; d += 4) *reinterpret_cast<f32x4 *>(dst + d) = f32x4{y[d], y[d + 1], y[d + 2], y[d + 3]};
+        }
+      }
+    }
+  }
+}
+
+template <int D, bool FP8, bool BF16ROWS, int MT>
+__global__ __launch_bounds__(64 * kWaves, kTileGroups) void attend_tile_kernel(AttendParams p, Cut cut) {
+  __shared__ u32x4 s_k[4 * 2 * (D / 32) * 64], s_v[4 * (D / 16) * 64];  // two tiles of two halves
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const Part<D> part{p.part, cut};
+  Stage<D, FP8> stage;
+  stage.init(tid);
+  Walk walk(p, cut, lane);
+  Seg sg;
+  int t0, t1;
+  while (walk.next(p, cut, lane, sg, t0, t1)) {
+    const Lens len = lens_of(p, sg.b);
+    const int first = walk.rb * cut.BM, rows = min(cut.BM, len.n * p.G - first);
+    if (rows <= 0) continue;
+    // the 16-row tiles in use, dealt out evenly, and from the other end in every other row block
+    const int place = walk.rb & 1 ? kWaves - 1 - wave : wave;
+    const int tiles = (rows + 15) >> 4, per = tiles / kWaves, extra = tiles % kWaves;
+    const int nt = per + (place < extra), mt0 = place * per + min(place, extra);
+    const bool whole = t0 == 0 && t1 == sg.steps;
+    const size_t slot = part.slot(walk.rb, walk.w, t0 == 0);
+    if (MT > 1 && nt == 2)
+      tile_pair<D, FP8, BF16ROWS, MT>(p, part, len, stage, s_k, s_v, sg.b, sg.h, first, rows, mt0, t0, t1, whole, slot, lane);
+    else if (nt == 1)
+      tile_pair<D, FP8, BF16ROWS, 1>(p, part, len, stage, s_k, s_v, sg.b, sg.h, first, rows, mt0, t0, t1, whole, slot, lane);
+    else
+      tile_pair<D, FP8, BF16ROWS, 0>(p, part, len, stage, s_k, s_v, sg.b, sg.h, first, rows, mt0, t0, t1, whole, slot, lane);
+  }
+}
+
+// ---- the join ------------------------------------------------------------------------------------
+
+// Joins the partial results of every pair that a cut goes through: workgroup (w, row block) looks at
+// the cut behind part w, and the first cut of a pair has it.  Sums of few parts: 32 (d = 128) or 16
+// lanes per row, the parts in order.  Of many (a long context's few rows): all lane groups of a
+// workgroup on one row at a time, the parts dealt out over them.  TH: many rows (tile kernel) are
+// joined by 1024 lanes in one workgroup, the few of the stream kernel by 256 in each of up to four.
+template <int D, bool BF16ROWS, int TH>
+__global__ __launch_bounds__(TH) void attend_join_kernel(AttendParams p, Cut cut) {
+  constexpr int LG = D / 4, GR = TH / LG;  // lanes per row, lane groups
+  constexpr int kFew = 4;
+  __shared__ float s_sum[GR][D], s_l[GR], s_top[TH / 64];
+  const int tid = threadIdx.x, lane = tid & 63, grp = tid / LG, e = tid % LG;
+  const int w0 = blockIdx.x, rb = blockIdx.y;
+  const long long per = head_steps(p, cut.keys, lane), share = share_of(per * p.c.H, cut);
+  const long long x = (w0 + 1) * share;
+  const Seg sg = locate(p, cut.keys, per, x, lane);
+  if (sg.b < 0 || sg.off == 0 || sg.off > share) return;  // a pair starts here, or its first cut is another
+  const int last = (int)((x - sg.off + sg.steps - 1) / share), parts = last - w0 + 1;
+  const Lens len = lens_of(p, sg.b);
+  const int first = rb * cut.BM, rows = min(cut.BM, len.n * p.G - first), Hq = p.c.H * p.G;
+  const Part<D> part{p.part, cut};
+  // part i: where part w0 of the list ends, then where the next ones begin
+  const auto slot = [&](int i) { return part.slot(rb, w0 + i, i == 0); };
+  const auto row_at = [&](int r) {
+    const int m = first + r;
+    return (((size_t)sg.b * p.R + m / p.G) * Hq + (size_t)sg.h * p.G + m % p.G) * D;
+  };
+  if (parts <= kFew) {
+    for (int r = blockIdx.z * GR + grp; r < rows; r += gridDim.z * GR) {
+      float st[kFew], sl[kFew], top = kNegInf, l = 0.f;
+      f32x4 sum[kFew], o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < kFew; ++i)
+        if (i < parts) {
+          const size_t at = slot(i);
+          st[i] = part.stat(at, r)[0];
+          sl[i] = part.stat(at, r)[1];
+          sum[i] = *reinterpret_cast<const f32x4 *>(part.sums(at, r) + 4 * e);
+        }
+#pragma unroll
+      for (int i = 0; i < kFew; ++i)
+        if (i < parts) top = fmaxf(top, st[i]);
+#pragma unroll
+      for (int i = 0; i < kFew; ++i)
+        if (i < parts) {
+          const float f = st[i] == top ? 1.f : __builtin_amdgcn_exp2f(st[i] - top);
+          l += f * sl[i];
+          o += f * sum[i];
+        }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] /= l;
+      if constexpr (BF16ROWS)
+        *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(p.o) + row_at(r) + 4 * e) = u32x2{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
+      else
+        *reinterpret_cast<f32x4 *>(static_cast<float *>(p.o) + row_at(r) + 4 * e) = o;
+    }
+    return;
+  }
+  for (int r = blockIdx.z; r < rows; r += gridDim.z) {
+    float top = kNegInf;
+    for (int i = tid; i < parts; i += TH) top = fmaxf(top, part.stat(slot(i), r)[0]);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+    if (lane == 0) s_top[tid >> 6] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < TH / 64; ++i) top = fmaxf(top, s_top[i]);
+    float l = 0.f;
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int i = grp; i < parts; i += GR) {
+      const float st = part.stat(slot(i), r)[0], f = st == top ? 1.f : __builtin_amdgcn_exp2f(st - top);
+      l += f * part.stat(slot(i), r)[1];
+      o += f * *reinterpret_cast<const f32x4 *>(part.sums(slot(i), r) + 4 * e);
+    }
+    *reinterpret_cast<f32x4 *>(&s_sum[grp][4 * e]) = o;
+    if (e == 0) s_l[grp] = l;
+    __syncthreads();
+    if (tid < D) {
+      float y = 0.f, ll = 0.f;
+#pragma unroll
+      for (int k = 0; k < GR; ++k) {
+        y += s_sum[k][tid];
+        ll += s_l[k];
+      }
+      store_o<BF16ROWS>(p.o, row_at(r) + tid, y / ll);
     }
     __syncthreads();
   }
-  const bool whole = it.count == 1;
-  if (wave == 0 && g == 0) {
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      s_m[0][16 * mt + c] = m_all[mt];
-      s_l[0][16 * mt + c] = l_all[mt];
-    }
-  }
-  __syncthreads();
-  const Part part{BM, D + 2};
-  float *mine = p.part + part.at(rb, h, p.c.H, units, it.slot + it.split);
-  for (int e = tid; e < BM * D; e += 64 * kWaves) {
-    const int r = e / D, d = e % D, m = rb * BM + r, t = m / p.G;
-    if (t >= len.n) break;
-    const float x = s_o[r * OST + d];
-    if (whole)
-      store_o<BF16ROWS>(p.o, (((size_t)b * p.R + t) * Hq + (size_t)h * p.G + m % p.G) * D + d, x / s_l[0][r]);
-    else
-      mine[r * (D + 2) + d] = x;
-  }
-  if (!whole && tid < BM) {
-    mine[tid * (D + 2) + D] = s_m[0][tid];
-    mine[tid * (D + 2) + D + 1] = s_l[0][tid];
-  }
 }
 
-// Joins the items of every request that was cut into more than one: one wave per query row.
-template <int D, bool BF16ROWS, int MT>
-__global__ __launch_bounds__(256) void attend_join_kernel(AttendParams p) {
-  constexpr int BM = 16 * MT, PL = D / 64;
-  const int lane = threadIdx.x & 63;
-  const int Hq = p.c.H * p.G;
-  const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (row >= (long long)p.B * p.R * Hq) return;
-  const int b = (int)(row / (p.R * Hq)), rem = (int)(row - (long long)b * p.R * Hq);
-  const int t = rem / Hq, hq = rem % Hq, h = hq / p.G, m = t * p.G + hq % p.G;
-  const int nrb = (p.R * p.G + BM - 1) / BM, units = nrb * p.c.H;
-  if (t >= lens_of(p, b).n) return;
-  const Item it = find_request(p, b, units, lane);
-  if (it.count < 2) return;  // written by its one item
-  const Part part{BM, D + 2};
-  const float *base = p.part + part.at(m / BM, h, p.c.H, units, it.slot) + (size_t)(m % BM) * (D + 2);
-  const size_t step = (size_t)BM * (D + 2);
-  float top = -__builtin_inff();
-  for (int s = lane; s < it.count; s += 64) top = fmaxf(top, base[s * step + D]);
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-  float x[PL], l = 0.f;
-#pragma unroll
-  for (int i = 0; i < PL; ++i) x[i] = 0.f;
-  for (int s = 0; s < it.count; ++s) {
-    const float *src = base + s * step;
-    const float ms = src[D], f = ms == top ? 1.f : __builtin_amdgcn_exp2f(ms - top);
-    l += f * src[D + 1];
-#pragma unroll
-    for (int i = 0; i < PL; ++i) x[i] += f * src[lane + 64 * i];
-  }
-#pragma unroll
-  for (int i = 0; i < PL; ++i) store_o<BF16ROWS>(p.o, (size_t)row * D + lane + 64 * i, x[i] / l);
+// ---- launches ------------------------------------------------------------------------------------
+
+// How a call is run: which kernel, and the cut.
+struct Shape {
+  int MT;  // 16-row tiles per wave; 0: the stream kernel
+  Cut cut;
+};
+
+Shape shape_of(int R, int G, int D, bool bf16_rows) {
+  const int tiles = (R * G + 15) / 16;
+  if (tiles == 1) return Shape{0, Cut{16, 1, kCUs * (D == 64 ? 4 : bf16_rows ? 3 : 2), kStreamKeys, kStreamLeast}};
+  const int most = kWaves * tile_most(bf16_rows);
+  // W: a multiple of 8, so that all workgroups (which come in rounds of 8) are resident at once
+  const int blocks = (tiles + most - 1) / most, each = (tiles + blocks - 1) / blocks;
+  return Shape{(each + kWaves - 1) / kWaves, Cut{16 * each, blocks, kCUs * kTileGroups / blocks / 8 * 8, kTileKeys, kTileLeast}};
 }
 
-// 16-row tiles per workgroup: the least that holds the query rows of a key-value head.
-int tiles_of(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
-
-template <int D, bool FP8, bool BF16ROWS, int MT>
-hipError_t launch_mt(const AttendParams &p, hipStream_t stream) {
-  const int nrb = (p.R * p.G + 16 * MT - 1) / (16 * MT), units = nrb * p.c.H;
-  hipLaunchKernelGGL((attend_kernel<D, FP8, BF16ROWS, MT>), dim3((unsigned)(units * items_most(p.B, units))),
-                     dim3(64 * kWaves), 0, stream, p);
-  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  const long long rows = (long long)p.B * p.R * p.c.H * p.G;
-  hipLaunchKernelGGL((attend_join_kernel<D, BF16ROWS, MT>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, p);
-  return hipGetLastError();
-}
+// Contexts that cannot be longer than this many positions go to one workgroup each: nothing to join.
+constexpr int kWholeStream = 1024, kWholeTile = 512;
 
 template <int D, bool FP8, bool BF16ROWS>
-hipError_t launch_rows(const AttendParams &p, hipStream_t stream) {
-  switch (tiles_of(p.R * p.G)) {
-    case 1: return launch_mt<D, FP8, BF16ROWS, 1>(p, stream);
-    case 2: return launch_mt<D, FP8, BF16ROWS, 2>(p, stream);
-    default: return launch_mt<D, FP8, BF16ROWS, 4>(p, stream);
-  }
+hipError_t launch_rows(AttendParams p, hipStream_t stream) {
+  const Shape s = shape_of(p.R, p.G, D, BF16ROWS);
+  const Cut &cut = s.cut;
+  p.whole = (long long)p.c.max_pages << p.c.shift <= (s.MT == 0 ? kWholeStream : kWholeTile);
+  // parts (or pairs) in rounds of 8, each for all row blocks
+  const long long parts = p.whole ? (long long)p.B * p.c.H : cut.W;
+  const dim3 grid((unsigned)((parts + 7) / 8 * 8 * cut.blocks)), block(64 * kWaves);
+  if (s.MT == 0)
+    hipLaunchKernelGGL((attend_stream_kernel<D, FP8, BF16ROWS>), grid, block, 0, stream, p);
+  else if (s.MT == 1)
+    hipLaunchKernelGGL((attend_tile_kernel<D, FP8, BF16ROWS, 1>), grid, block, 0, stream, p, cut);
+  else if constexpr (BF16ROWS)
+    hipLaunchKernelGGL((attend_tile_kernel<D, FP8, BF16ROWS, 2>), grid, block, 0, stream, p, cut);
+  if (hipError_t e = hipGetLastError(); e != hipSuccess || p.whole) return e;
+  if (s.MT == 0)
+    hipLaunchKernelGGL((attend_join_kernel<D, BF16ROWS, 256>), dim3((unsigned)(cut.W - 1), 1, (unsigned)min(p.R * p.G, 4)),
+                       dim3(256), 0, stream, p, cut);
+  else
+    hipLaunchKernelGGL((attend_join_kernel<D, BF16ROWS, 1024>), dim3((unsigned)(cut.W - 1), (unsigned)cut.blocks),
+                       dim3(1024), 0, stream, p, cut);
+  return hipGetLastError();
 }
 
 template <int D>
@@ -561,17 +995,19 @@ hipError_t launch_d(const AttendParams &p, hipStream_t stream) {
 
 }  // namespace
 
-size_t attend_workspace(int B, int R, int G, int H, int D) {
-  (void)B;  // the items of a batch are bounded by the chip, not by the batch
-  const int BM = 16 * tiles_of(R * G), units = (R * G + BM - 1) / BM * H;
-  return (size_t)units * slots_most(units) * BM * (D + 2) * sizeof(float);
+size_t attend_workspace(int R, int G, int D) {
+  size_t most = 0;  // whichever type the rows have
+  for (int bf16_rows = 0; bf16_rows < 2; ++bf16_rows) {
+    const Shape s = shape_of(R, G, D, bf16_rows);
+    const size_t bytes = (size_t)2 * s.cut.blocks * s.cut.W * s.cut.BM * (D + 2) * sizeof(float);
+    most = bytes > most ? bytes : most;
+  }
+  return most;
 }
 
 bool attend_fits(int B, int R, int G, int H) {
-  const int BM = 16 * tiles_of(R * G);
-  const long long units = (long long)((R * G + BM - 1) / BM) * H;
-  const long long rows = (long long)B * R * G;  // < 2^42: no overflow in the product below
-  return units < (1LL << 24) && units * (kItems + 1LL + B) < 0x7fffffffLL && rows * H / 4 < 0x7ffffffeLL;
+  // one workgroup per (request, head, row block) at most, in rounds of 8; 16 rows a block at least
+  return (long long)B * H + 8 < 0x7fffffffLL / ((R * G + 15) / 16);
 }
 
 hipError_t launch_attend(const AttendParams &p, hipStream_t stream) {

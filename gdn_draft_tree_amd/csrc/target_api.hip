@@ -116,7 +116,7 @@ GDNTREE_EXPORT gdntree_status gdntree_cache_commit(gdntree_cache cache, const in
 
 GDNTREE_EXPORT size_t gdntree_attend_workspace(int B, int R, int H_q, int H_kv, int d) {
   if (!attend_sizes(B, R, H_q, H_kv, d) || !attend_limits(R, H_q, H_kv, d)) return 0;
-  return attend_workspace(B, R, H_q / H_kv, H_kv, d);
+  return attend_workspace(R, H_q / H_kv, d);
 }
 
 GDNTREE_EXPORT gdntree_status gdntree_attend(gdntree_cache cache, int layer, const int32_t *table, int max_pages,

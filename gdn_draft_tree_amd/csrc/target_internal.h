@@ -57,9 +57,10 @@ struct AttendParams {
   float scale_log2;                  // scale * log2(e)
   int B, R, G, D;                    // G: query heads per key-value head
   int fp8, rows_bf16;
+  bool whole = false;                // one workgroup per (request, head, row block): nothing to join
 };
 hipError_t launch_attend(const AttendParams &p, hipStream_t stream);
-size_t attend_workspace(int B, int R, int G, int H, int D);
+size_t attend_workspace(int R, int G, int D);
 bool attend_fits(int B, int R, int G, int H);  // the launches' grids
 
 struct SampleParams {

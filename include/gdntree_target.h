@@ -123,8 +123,8 @@ gdntree_status gdntree_cache_commit(gdntree_cache cache, const int32_t *table, i
  * bf16 rows: exact products, fp32 sums and softmax statistics; the softmax weights enter the
  * product with the values rounded to bf16, and o is rounded once.  fp32 rows: q and the weights
  * are split into three bf16 parts, so that every product is exact and the sums are fp32.
- * A request whose ctx_len is negative, whose positions exceed max_pages * page_size, or which
- * meets a page id outside [0, pages) gets NaN in its rows < n_rows[b].
+ * A request whose ctx_len is negative, whose positions exceed max_pages * page_size or 2^28 - 65,
+ * or which meets a page id outside [0, pages) gets NaN in its rows < n_rows[b].
  * Limits: R <= 65, H_q a multiple of H_kv, H_q / H_kv <= 16.
  */
 size_t gdntree_attend_workspace(int B, int R, int H_q, int H_kv, int d);
