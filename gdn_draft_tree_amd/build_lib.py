@@ -19,6 +19,9 @@ TARGET_LIB = os.path.join(HERE, "libgdntree_target.so")
 # the benchmark's streaming probe, in a library of its own (not part of the path's ABI)
 PROBE_SOURCES = ["stream_probe.hip"]
 PROBE_LIB = os.path.join(HERE, "libgdntree_probe.so")
+# the torch binding of libgdntree_target.so (host code: g++ against torch's headers)
+CALLS_SOURCE = "target_calls.cpp"
+CALLS_LIB = os.path.join(HERE, "_calls.so")
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
     "-fvisibility=hidden",
@@ -30,7 +33,29 @@ FLAGS = [
 def build(verbose: bool = False, extra: list[str] | None = None) -> str:
     _build_one(PROBE_LIB, PROBE_SOURCES, verbose, extra)
     _build_one(TARGET_LIB, TARGET_SOURCES, verbose, extra)
+    _build_calls(verbose)
     return _build_one(LIB, SOURCES, verbose, extra)
+
+
+def _build_calls(verbose: bool) -> None:
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    lib = os.path.join(root, "lib")
+    tmp = CALLS_LIB + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-D__HIP_PLATFORM_AMD__",
+           "-isystem", os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include"), f"-I{os.path.join(root, 'include')}",
+           f"-I{sysconfig.get_paths()['include']}", os.path.join(CSRC, CALLS_SOURCE), "-o", tmp, f"-L{HERE}",
+           "-l:libgdntree_target.so", "-Wl,-rpath,$ORIGIN", f"-L{lib}", f"-Wl,-rpath,{lib}", "-lc10", "-ltorch_cpu",
+           "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed ({res.returncode}):\n{res.stderr}")
+    os.replace(tmp, CALLS_LIB)
 
 
 def _build_one(lib: str, sources: list[str], verbose: bool, extra: list[str] | None) -> str:

@@ -962,12 +962,13 @@ Shape shape_of(int R, int G, int D, bool bf16_rows) {
 
 // Contexts that cannot be longer than this many positions go to one workgroup each: nothing to join.
 constexpr int kWholeStream = 1024, kWholeTile = 512;
+bool is_whole(const Shape &s, long long positions) { return positions <= (s.MT == 0 ? kWholeStream : kWholeTile); }
 
 template <int D, bool FP8, bool BF16ROWS>
 hipError_t launch_rows(AttendParams p, hipStream_t stream) {
   const Shape s = shape_of(p.R, p.G, D, BF16ROWS);
   const Cut &cut = s.cut;
-  p.whole = (long long)p.c.max_pages << p.c.shift <= (s.MT == 0 ? kWholeStream : kWholeTile);
+  p.whole = is_whole(s, (long long)p.c.max_pages << p.c.shift);
   // parts (or pairs) in rounds of 8, each for all row blocks
   const long long parts = p.whole ? (long long)p.B * p.c.H : cut.W;
   const dim3 grid((unsigned)((parts + 7) / 8 * 8 * cut.blocks)), block(64 * kWaves);
@@ -995,10 +996,11 @@ hipError_t launch_d(const AttendParams &p, hipStream_t stream) {
 
 }  // namespace
 
-size_t attend_workspace(int R, int G, int D) {
+size_t attend_workspace(int R, int G, int D, long long positions) {
   size_t most = 0;  // whichever type the rows have
   for (int bf16_rows = 0; bf16_rows < 2; ++bf16_rows) {
     const Shape s = shape_of(R, G, D, bf16_rows);
+    if (is_whole(s, positions)) continue;
     const size_t bytes = (size_t)2 * s.cut.blocks * s.cut.W * s.cut.BM * (D + 2) * sizeof(float);
     most = bytes > most ? bytes : most;
   }

@@ -114,9 +114,9 @@ GDNTREE_EXPORT gdntree_status gdntree_cache_commit(gdntree_cache cache, const in
   return GDNTREE_OK;
 }
 
-GDNTREE_EXPORT size_t gdntree_attend_workspace(int B, int R, int H_q, int H_kv, int d) {
-  if (!attend_sizes(B, R, H_q, H_kv, d) || !attend_limits(R, H_q, H_kv, d)) return 0;
-  return attend_workspace(R, H_q / H_kv, d);
+GDNTREE_EXPORT size_t gdntree_attend_workspace(int R, int H_q, int H_kv, int d, int max_pages, int page_size) {
+  if (!attend_sizes(1, R, H_q, H_kv, d) || !attend_limits(R, H_q, H_kv, d) || max_pages <= 0 || page_size <= 0) return 0;
+  return attend_workspace(R, H_q / H_kv, d, (long long)max_pages * page_size);
 }
 
 GDNTREE_EXPORT gdntree_status gdntree_attend(gdntree_cache cache, int layer, const int32_t *table, int max_pages,
@@ -124,13 +124,14 @@ GDNTREE_EXPORT gdntree_status gdntree_attend(gdntree_cache cache, int layer, con
                                              int R, int H_q, gdntree_dtype dtype, const void *q, float scale, void *o,
                                              void *workspace, size_t workspace_bytes, hipStream_t stream) {
   if (gdntree_status st = check_cache(cache, table, max_pages); st != GDNTREE_OK) return st;
-  if (!ctx_len || !q || !o || !workspace || !aligned(q) || !aligned(o) || !aligned(workspace)) return GDNTREE_ERR_ARG;
+  if (!ctx_len || !q || !o || !aligned(q) || !aligned(o) || !aligned(workspace)) return GDNTREE_ERR_ARG;
   if (layer < 0 || layer >= cache.L || !attend_sizes(B, R, H_q, cache.H_kv, cache.d) || !dtype_ok(dtype))
     return GDNTREE_ERR_ARG;
   if (!(scale > 0.f) || !(scale < INFINITY)) return GDNTREE_ERR_ARG;
   if (!attend_limits(R, H_q, cache.H_kv, cache.d) || !attend_fits(B, R, H_q / cache.H_kv, cache.H_kv))
     return GDNTREE_ERR_UNSUPPORTED;
-  if (workspace_bytes < gdntree_attend_workspace(B, R, H_q, cache.H_kv, cache.d)) return GDNTREE_ERR_ARG;
+  const size_t need = gdntree_attend_workspace(R, H_q, cache.H_kv, cache.d, max_pages, cache.page_size);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return GDNTREE_ERR_ARG;
   if (gdntree_status st = device_ok(); st != GDNTREE_OK) return st;
   AttendParams p;
   p.c = view(cache, layer, table, max_pages);

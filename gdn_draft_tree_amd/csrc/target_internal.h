@@ -60,7 +60,7 @@ struct AttendParams {
   bool whole = false;                // one workgroup per (request, head, row block): nothing to join
 };
 hipError_t launch_attend(const AttendParams &p, hipStream_t stream);
-size_t attend_workspace(int R, int G, int D);
+size_t attend_workspace(int R, int G, int D, long long positions);  // positions: most a table holds
 bool attend_fits(int B, int R, int G, int H);  // the launches' grids
 
 struct SampleParams {

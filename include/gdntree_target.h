@@ -119,7 +119,8 @@ gdntree_status gdntree_cache_commit(gdntree_cache cache, const int32_t *table, i
  *   anc      u64 [B][R] or NULL
  *   n_rows   i32 [B] or NULL (R rows each); a request with n_rows outside [1, R] gets no output
  *   scale    > 0, finite (d^-1/2 usually)
- *   workspace  at least gdntree_attend_workspace(...) bytes, 16-byte aligned
+ *   workspace  at least gdntree_attend_workspace(...) bytes, 16-byte aligned (NULL where that is 0:
+ *              contexts that the table's width keeps short are not split)
  * bf16 rows: exact products, fp32 sums and softmax statistics; the softmax weights enter the
  * product with the values rounded to bf16, and o is rounded once.  fp32 rows: q and the weights
  * are split into three bf16 parts, so that every product is exact and the sums are fp32.
@@ -127,7 +128,7 @@ gdntree_status gdntree_cache_commit(gdntree_cache cache, const int32_t *table, i
  * or which meets a page id outside [0, pages) gets NaN in its rows < n_rows[b].
  * Limits: R <= 65, H_q a multiple of H_kv, H_q / H_kv <= 16.
  */
-size_t gdntree_attend_workspace(int B, int R, int H_q, int H_kv, int d);
+size_t gdntree_attend_workspace(int R, int H_q, int H_kv, int d, int max_pages, int page_size);
 gdntree_status gdntree_attend(gdntree_cache cache, int layer, const int32_t *table, int max_pages,
                               const int32_t *ctx_len, const uint64_t *anc, const int32_t *n_rows, int B, int R,
                               int H_q, gdntree_dtype dtype, const void *q, float scale, void *o,

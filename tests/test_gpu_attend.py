@@ -256,7 +256,8 @@ def test_binding_refusals():
     for bad in (dict(q=q.half()), dict(q=q.transpose(1, 2)), dict(q=q[:, :, :, :32]), dict(ctx=ctx.long()),
                 dict(table=table[:1]), dict(n_rows=i32([3, 3]), tree=tree), dict(o=q.float()),
                 dict(workspace=torch.empty(64, dtype=torch.uint8)), dict(layer=1), dict(layer=-1), dict(scale=0.0),
-                dict(workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))):
+                # contexts that may be long need the whole workspace (short ones, as above, need none)
+                dict(workspace=torch.empty(64, dtype=torch.uint8, device="cuda"), table=table.repeat(1, 80))):
         a = dict(q=q, ctx=ctx, table=table, layer=0, tree=None, n_rows=None, scale=None, o=None, workspace=None)
         a.update(bad)
         with pytest.raises((ValueError, g.GdnTreeError)):

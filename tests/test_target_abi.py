@@ -70,23 +70,24 @@ def test_cache_commit_refuses(kw, expect):
 
 
 @pytest.mark.parametrize("kw,expect", [
-    (dict(ctx=None), 1), (dict(q=None), 1), (dict(o=None), 1), (dict(ws=None), 1), (dict(q=FAKE + 8), 1),
+    (dict(ctx=None), 1), (dict(q=None), 1), (dict(o=None), 1), (dict(ws=None, width=100), 1), (dict(q=FAKE + 8), 1),
     (dict(o=FAKE + 2), 1), (dict(ws=FAKE + 4), 1), (dict(layer=2), 1), (dict(B=0), 1), (dict(R=0), 1), (dict(Hq=0), 1),
     (dict(dt=5), 1), (dict(scale=0.0), 1), (dict(scale=-1.0), 1), (dict(scale=float("nan")), 1),
-    (dict(scale=float("inf")), 1), (dict(size=16), 1), (dict(R=66), 2), (dict(Hq=6), 2), (dict(Hq=68), 2),
+    (dict(scale=float("inf")), 1), (dict(size=16, width=100), 1), (dict(R=66), 2), (dict(Hq=6), 2), (dict(Hq=68), 2),
     (dict(B=(1 << 31) - 1), 2),
 ])
 def test_attend_refuses(kw, expect):
-    a = dict(layer=0, ctx=FAKE, B=2, R=3, Hq=8, dt=1, q=FAKE, scale=0.1, o=FAKE, ws=FAKE, size=1 << 40)
+    a = dict(layer=0, width=4, ctx=FAKE, B=2, R=3, Hq=8, dt=1, q=FAKE, scale=0.1, o=FAKE, ws=FAKE, size=1 << 40)
     a.update(kw)
-    assert L.gdntree_attend(cache(), a["layer"], FAKE, 4, a["ctx"], None, None, a["B"], a["R"], a["Hq"], a["dt"],
+    assert L.gdntree_attend(cache(), a["layer"], FAKE, a["width"], a["ctx"], None, None, a["B"], a["R"], a["Hq"], a["dt"],
                             a["q"], a["scale"], a["o"], a["ws"], a["size"], None) == expect
 
 
 def test_workspace_sizes():
-    assert L.gdntree_attend_workspace(2, 66, 8, 4, 128) == 0 and L.gdntree_attend_workspace(2, 3, 6, 4, 128) == 0
-    assert L.gdntree_attend_workspace(0, 3, 8, 4, 128) == 0
-    assert 0 < L.gdntree_attend_workspace(1, 1, 8, 8, 64) < L.gdntree_attend_workspace(1, 65, 8, 8, 128) < 1 << 28
+    W = L.gdntree_attend_workspace
+    assert W(66, 8, 4, 128, 100, 64) == 0 and W(3, 6, 4, 128, 100, 64) == 0 and W(0, 8, 4, 128, 100, 64) == 0
+    assert 0 < W(1, 8, 8, 64, 100, 64) < W(65, 8, 8, 128, 100, 64) < 1 << 28
+    assert W(1, 8, 8, 64, 64, 16) == 0 and W(65, 8, 8, 128, 32, 16) == 0      # contexts too short to split
     assert L.gdntree_accept_sample_workspace(1, 65, 100) == 0
     assert L.gdntree_accept_sample_workspace(1, 64, (1 << 24) + 1) == 0
     assert 0 < L.gdntree_accept_sample_workspace(1, 1, 1) < L.gdntree_accept_sample_workspace(32, 64, 151936) < 1 << 22
@@ -130,6 +131,6 @@ def test_binding_refuses_host_tensors_and_bad_caches():
     with pytest.raises(ValueError):
         g.gdntree_cache_commit(kv, table, i32, i32, torch.zeros(1, 5, dtype=torch.int32), 4)
     with pytest.raises(ValueError):
-        g.gdntree_accept_sample(None, torch.zeros(1, 5, 9), torch.ones(1), torch.zeros(1, 5), 4)
+        g.gdntree_accept_sample(g.Tree.empty(1, 4, "cpu"), torch.zeros(1, 5, 9), torch.ones(1), torch.zeros(1, 5), 4)
     with pytest.raises(ValueError):
         g.KVCache.empty(1, 4, 4, 16, 64, dtype=torch.float16, device="cpu")
