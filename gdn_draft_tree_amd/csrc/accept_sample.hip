@@ -127,7 +127,8 @@ __device__ __forceinline__ float rebase(float m, float top, float c) {
   return (float)((finite(r) ? (double)r : (double)m * c) - (double)top * c);
 }
 
-// Eight logits as they are stored: one 16-byte load (bf16) or two.
+// Eight logits as they are stored: one 16-byte load (bf16) or two, past the caches (each logit is read
+// once: 91 us against 103 us for 575 MB).
 template <bool BF16>
 struct Raw8 {
   u32x4 w[BF16 ? 1 : 2];
@@ -143,8 +144,8 @@ __device__ __forceinline__ Raw8<BF16> load_raw8(const unsigned char *base, int e
   constexpr int ES = BF16 ? 2 : 4;
   Raw8<BF16> r;
   if (e >= pad && e + 8 <= end) {
-    r.w[0] = *reinterpret_cast<const u32x4 *>(base + (size_t)e * ES);
-    if constexpr (!BF16) r.w[1] = *reinterpret_cast<const u32x4 *>(base + (size_t)e * ES + 16);
+    r.w[0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(base + (size_t)e * ES));
+    if constexpr (!BF16) r.w[1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(base + (size_t)e * ES + 16));
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {

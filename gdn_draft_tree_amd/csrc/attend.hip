@@ -365,6 +365,13 @@ constexpr int kStreamLeast = 8;  // steps per workgroup: two per wave
 template <int D, bool BF16ROWS>
 constexpr int stream_groups() { return D == 64 ? 4 : BF16ROWS ? 3 : 2; }
 
+// A load past the caches: nothing else reads these rows (97 us against 105 us for one row over
+// 131,000 positions, 537 MB).
+template <class T>
+__device__ __forceinline__ T once(const unsigned char *src) {
+  return __builtin_nontemporal_load(reinterpret_cast<const T *>(src));
+}
+
 template <int D, bool FP8, bool BF16ROWS>
 __global__ __launch_bounds__(64 * kWaves, (stream_groups<D, BF16ROWS>())) void attend_stream_kernel(AttendParams p) {
   constexpr int KS = D / 32;               // 32-channel steps of the scores' product
@@ -420,15 +427,15 @@ __global__ __launch_bounds__(64 * kWaves, (stream_groups<D, BF16ROWS>())) void a
           const int pos = min(pos0 + 8 * (c >> 2) + 4 * hh + (c & 3), total - 1);
           const unsigned char *src = p.c.k + p.c.row(pgk, h, pos) * D + 16 * g;
 #pragma unroll
-          for (int s2 = 0; s2 < KS / 2; ++s2) raw[hh][s2] = *reinterpret_cast<const u32x4 *>(src + 64 * s2);
+          for (int s2 = 0; s2 < KS / 2; ++s2) raw[hh][s2] = once<u32x4>(src + 64 * s2);
         }
         u32x2 vraw[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int pos = min(pos0 + 8 * g + e, total - 1);
           const unsigned char *src = p.c.v + p.c.row(pgv, h, pos) * D + DV * c;
-          if constexpr (DV == 8) vraw[e] = *reinterpret_cast<const u32x2 *>(src);
-          else vraw[e] = u32x2{*reinterpret_cast<const unsigned *>(src), 0u};
+          if constexpr (DV == 8) vraw[e] = once<u32x2>(src);
+          else vraw[e] = u32x2{once<unsigned>(src), 0u};
         }
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
@@ -455,16 +462,16 @@ __global__ __launch_bounds__(64 * kWaves, (stream_groups<D, BF16ROWS>())) void a
           const int pos = min(pos0 + 8 * (c >> 2) + 4 * hh + (c & 3), total - 1);
           const unsigned char *src = p.c.k + p.c.row(pgk, h, pos) * (2 * D) + 16 * g;
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks) kr[hh][ks] = *reinterpret_cast<const u32x4 *>(src + 64 * ks);
+          for (int ks = 0; ks < KS; ++ks) kr[hh][ks] = once<u32x4>(src + 64 * ks);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int pos = min(pos0 + 8 * g + e, total - 1);
           const unsigned char *src = p.c.v + p.c.row(pgv, h, pos) * (2 * D) + 2 * DV * c;
           if constexpr (DV == 8) {
-            vr[e] = *reinterpret_cast<const u32x4 *>(src);
+            vr[e] = once<u32x4>(src);
           } else {
-            const u32x2 y = *reinterpret_cast<const u32x2 *>(src);
+            const u32x2 y = once<u32x2>(src);
             vr[e] = u32x4{y[0], y[1], 0u, 0u};
           }
         }

@@ -59,9 +59,7 @@ gdntree_status rows_call(const gdntree_cache &cache, int layer, const int32_t *t
   if (gdntree_status st = check_cache(cache, table, max_pages); st != GDNTREE_OK) return st;
   if (!start || !k || !v || !aligned(k) || !aligned(v)) return GDNTREE_ERR_ARG;
   if (layer < 0 || layer >= cache.L || B <= 0 || R <= 0 || !dtype_ok(dtype)) return GDNTREE_ERR_ARG;
-  // 256 lanes hold 256 * 8 / d rows
-  const __int128 threads = (__int128)B * R * cache.H_kv * (cache.d / 8);
-  if (threads / 256 >= 0x7ffffffeLL) return GDNTREE_ERR_UNSUPPORTED;
+  if ((__int128)B * R * cache.H_kv > 0x7fffffffLL - 65536) return GDNTREE_ERR_UNSUPPORTED;  // rows, in 32 bits
   if (gdntree_status st = device_ok(); st != GDNTREE_OK) return st;
   RowsParams p;
   p.c = view(cache, layer, table, max_pages);
