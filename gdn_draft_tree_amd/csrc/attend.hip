@@ -63,6 +63,14 @@ __device__ __forceinline__ unsigned pack_bf16(float lo, float hi) {
   return __builtin_bit_cast(unsigned, r);
 }
 
+// A value that is only known inside the branch it is taken in: without this the compiler computes
+// both sides of a rare branch and selects.
+template <class T>
+__device__ __forceinline__ T rarely(T x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 // Two e4m3 codes (the low or the high half of w) times a power of two, as bf16.
 template <bool HIGH>
 __device__ __forceinline__ unsigned fp8_pair(unsigned w, float s) {
@@ -489,13 +497,14 @@ __global__ __launch_bounds__(64 * kWaves, (stream_groups<D, BF16ROWS>())) void a
           for (int i = NQ - 1; i >= 0; --i) s[hh] = mfma(kr[hh][ks], q.f[0][ks][i], s[hh]);
       }
       if (masked) {
-        mask_scores(s, q.see[0], pos0 + 8 * g - len.ctx);
+        mask_scores(s, q.see[0], rarely(pos0 + 8 * g - len.ctx));
 #pragma unroll
         for (int e = 0; e < 8; ++e)
 #pragma unroll
           for (int w = 0; w < DV / 2; ++w) {
-            odd = odd || odd_bf16_pair(vr[e][w]);
-            vr[e][w] = clean_pair(vr[e][w]);
+            const unsigned x = rarely(vr[e][w]);
+            odd = odd || odd_bf16_pair(x);
+            vr[e][w] = clean_pair(x);
           }
       }
       const float top = Running<DV>::top_of(s, p.scale_log2);
@@ -587,6 +596,12 @@ constexpr int kTileLeast = 4;  // tiles per workgroup
 constexpr int kTileGroups = 2;
 constexpr int tile_most(bool bf16_rows) { return bf16_rows ? 2 : 1; }
 
+// Where a lane's 16 bytes lie within the 16 of its group, so that the 8 consecutive lanes of a store,
+// which have two rows of four groups (keys) or four channels of two products (values), hit 8 places
+// that differ mod 8, as the 8 consecutive lanes of a load do.
+__device__ __forceinline__ int swap_k(int r, int g) { return r ^ (2 * g); }
+__device__ __forceinline__ int swap_v(int c, int j) { return c ^ (j & 4); }
+
 // One workgroup's staging of a 64-key tile: what a thread holds between loading and storing it.
 // each of 256 (d = 128) or 128 threads has eight keys of four value channels, and each of 256 a quarter
 // of one key row (all its 16-byte chunks of one residue mod 4).
@@ -660,9 +675,13 @@ struct Stage {
         } else {
           x[e] = v[e];
         }
-        if (masked) {
-          odd = odd || odd_bf16_pair(x[e][0]) || odd_bf16_pair(x[e][1]);
-          x[e] = u32x2{clean_pair(x[e][0]), clean_pair(x[e][1])};
+      }
+      if (masked) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const unsigned a = rarely(x[e][0]), b = rarely(x[e][1]);
+          odd = odd || odd_bf16_pair(a) || odd_bf16_pair(b);
+          x[e] = u32x2{clean_pair(a), clean_pair(b)};
         }
       }
 #pragma unroll
@@ -672,7 +691,7 @@ struct Stage {
         for (int k2 = 0; k2 < 4; ++k2)
           y[k2] = __builtin_amdgcn_perm(x[2 * k2 + 1][j >> 1], x[2 * k2][j >> 1], j & 1 ? 0x07060302u : 0x05040100u);
         const int ch = 4 * cc + j;
-        sv[((kg >> 2) * DV + ch % DV) * 64 + (kg & 3) * 16 + ch / DV] = y;
+        sv[((kg >> 2) * DV + ch % DV) * 64 + (kg & 3) * 16 + swap_v(ch / DV, ch % DV)] = y;
       }
     }
     const int at = ((row >> 5) * 2 + ((row >> 2) & 1)) * KS, r = 4 * ((row & 31) >> 3) + (row & 3);
@@ -683,11 +702,11 @@ struct Stage {
         const int q = quarter + 4 * i;  // channels 16 q .. 16 q + 15
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf)
-          sk[(at + (q >> 1)) * 64 + (2 * (q & 1) + hf) * 16 + r] =
+          sk[(at + (q >> 1)) * 64 + (2 * (q & 1) + hf) * 16 + swap_k(r, 2 * (q & 1) + hf)] =
               u32x4{fp8_pair<false>(k[i][2 * hf], s), fp8_pair<true>(k[i][2 * hf], s),
                     fp8_pair<false>(k[i][2 * hf + 1], s), fp8_pair<true>(k[i][2 * hf + 1], s)};
       } else {
-        sk[(at + i) * 64 + quarter * 16 + r] = k[i];
+        sk[(at + i) * 64 + quarter * 16 + swap_k(r, quarter)] = k[i];
       }
     }
   }
@@ -704,7 +723,7 @@ __device__ __forceinline__ void tile_half(const u32x4 *sk, const u32x4 *sv, cons
   for (int mt = 0; mt < NT; ++mt) s[mt][0] = s[mt][1] = f32x4{0.f, 0.f, 0.f, 0.f};
   u32x4 kf[2 * KS], vf[DV];
 #pragma unroll
-  for (int i = 0; i < 2 * KS; ++i) kf[i] = sk[i * 64 + lane];
+  for (int i = 0; i < 2 * KS; ++i) kf[i] = sk[i * 64 + 16 * g + swap_k(lane & 15, g)];
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int ks = 0; ks < KS; ++ks)
@@ -716,11 +735,13 @@ __device__ __forceinline__ void tile_half(const u32x4 *sk, const u32x4 *sv, cons
         for (int i = NQ - 1; i >= 0; --i) s[mt][hh] = mfma(kf[hh * KS + ks], q.f[mt][ks][i], s[mt][hh]);
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-  for (int d = 0; d < DV; ++d) vf[d] = sv[d * 64 + lane];
+  for (int d = 0; d < DV; ++d) vf[d] = sv[d * 64 + 16 * g + swap_v(lane & 15, d)];
   __builtin_amdgcn_sched_barrier(0);
-  if (slot0 + 32 > 0)  // new rows, or positions past the last one
+  if (slot0 + 32 > 0) {  // new rows, or positions past the last one
+    const int from = rarely(slot0 + 8 * g);
 #pragma unroll
-    for (int mt = 0; mt < NT; ++mt) mask_scores(s[mt], q.see[mt], slot0 + 8 * g);
+    for (int mt = 0; mt < NT; ++mt) mask_scores(s[mt], q.see[mt], from);
+  }
   float top[NT];
   bool more = false;
 #pragma unroll
@@ -728,9 +749,10 @@ __device__ __forceinline__ void tile_half(const u32x4 *sk, const u32x4 *sv, cons
     top[mt] = Running<DV>::top_of(s[mt], scale_log2);
     more = more || top[mt] > run[mt].m + kLazy;
   }
-  if (__any(more))
+  if (__any(more)) {
 #pragma unroll
-    for (int mt = 0; mt < NT; ++mt) run[mt].raise(top[mt]);
+    for (int mt = 0; mt < NT; ++mt) run[mt].raise(rarely(top[mt]));
+  }
   u32x4 pf[NT][NQ];
 #pragma unroll
   for (int mt = 0; mt < NT; ++mt) {
