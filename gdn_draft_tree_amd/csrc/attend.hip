@@ -19,8 +19,7 @@
 //    consecutive channels (whole rows, coalesced), and interleaves the keys' 16-bit halves in
 //    registers (v_perm).
 // The softmax is thus per lane except for the maximum, and that is only joined across lanes when a
-// score exceeds the running one by 2^8: until then the old maximum serves (weights up to 2^8 in
-// fp32 and bf16 lose nothing).
+// score exceeds the running one by far: until then the old maximum serves.
 //
 // Two kernels, by the number of query rows a key-value head has:
 //  * at most 16 (a new token of up to 16 heads a group): the cache's bytes are all there is.
@@ -48,7 +47,7 @@ namespace gdntree {
 namespace {
 
 constexpr int kCUs = 256;
-constexpr float kLazy = 8.f;      // how far (log2) a score may exceed the running maximum
+constexpr float kNone = -3.402823466e38f;  // the running maximum before any score: the lowest float
 constexpr float kNegInf = -__builtin_inff();
 constexpr int kMaxPos = 1 << 28;  // positions per request
 
@@ -264,23 +263,32 @@ struct Queries {
 
 // Running softmax of one 16-query tile: this lane's column, joined over its four lane groups in m
 // only (l is the lane's own until the end).
+//
+// The maximum is looked at through the weights: 8 of them and their sum are computed with the running
+// maximum as it is, and only if some lane's sum exceeds 2^8 (or is not a number) is the maximum
+// found, joined over the lanes, and the 8 weights computed again.  Weights up to 2^8 lose nothing in
+// fp32 or bf16.  Before anything is seen m is kNone, with which any finite score's weight overflows.
 template <int DV>
 struct Running {
   float m, l;
   f32x4 acc[DV];
   __device__ __forceinline__ void clear() {
-    m = kNegInf;
+    m = kNone;
     l = 0.f;
 #pragma unroll
     for (int d = 0; d < DV; ++d) acc[d] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  // The largest of 8 scores (already masked), in the exponent's units.
-  static __device__ __forceinline__ float top_of(const f32x4 s[2], float c) {
-    return c * fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
-                     fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
+  // The weights of 8 scores (already masked), and their sum.
+  __device__ __forceinline__ float weights(const f32x4 s[2], float c, float w[8]) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e >> 2][e & 3], c, -m));
+    return ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
   }
-  // Moves the maximum up to at least top, over the column's four lane groups.
-  __device__ __forceinline__ void raise(float top) {
+  static __device__ __forceinline__ bool fits(float sum) { return sum <= 256.f; }
+  // Moves the maximum up to that of the 8 scores, over the column's four lane groups.
+  __device__ __forceinline__ void raise(const f32x4 s[2], float c) {
+    float top = c * fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
+                          fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
     top = fmaxf(top, __shfl_xor(top, 16));
     top = fmaxf(top, __shfl_xor(top, 32));
     const float next = fmaxf(m, top);
@@ -289,12 +297,6 @@ struct Running {
     l *= f;
 #pragma unroll
     for (int d = 0; d < DV; ++d) acc[d] *= f;
-  }
-  __device__ __forceinline__ void weights(const f32x4 s[2], float c, float w[8]) {
-    const float ms = m == kNegInf ? 0.f : m;  // a column that sees nothing yet
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e >> 2][e & 3], c, -ms));
-    l += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
   }
 };
 
@@ -507,10 +509,12 @@ __global__ __launch_bounds__(64 * kWaves, (stream_groups<D, BF16ROWS>())) void a
             vr[e][w] = clean_pair(x);
           }
       }
-      const float top = Running<DV>::top_of(s, p.scale_log2);
-      if (__any(top > run[0].m + kLazy)) run[0].raise(top);
-      float w[8];
-      run[0].weights(s, p.scale_log2, w);
+      float w[8], sum = run[0].weights(s, p.scale_log2, w);
+      if (__any(!Running<DV>::fits(sum))) {
+        run[0].raise(s, rarely(p.scale_log2));
+        sum = run[0].weights(s, p.scale_log2, w);
+      }
+      run[0].l += sum;
       u32x4 pf[NQ];
       weight_operand<BF16ROWS>(w, pf);
 #pragma unroll
@@ -742,30 +746,31 @@ __device__ __forceinline__ void tile_half(const u32x4 *sk, const u32x4 *sv, cons
 #pragma unroll
     for (int mt = 0; mt < NT; ++mt) mask_scores(s[mt], q.see[mt], from);
   }
-  float top[NT];
-  bool more = false;
+  float w[NT][8], sum[NT];
+  bool ok = true;
 #pragma unroll
   for (int mt = 0; mt < NT; ++mt) {
-    top[mt] = Running<DV>::top_of(s[mt], scale_log2);
-    more = more || top[mt] > run[mt].m + kLazy;
+    sum[mt] = run[mt].weights(s[mt], scale_log2, w[mt]);
+    ok = ok && Running<DV>::fits(sum[mt]);
   }
-  if (__any(more)) {
+  if (__any(!ok)) {
+    const float c = rarely(scale_log2);
 #pragma unroll
-    for (int mt = 0; mt < NT; ++mt) run[mt].raise(rarely(top[mt]));
+    for (int mt = 0; mt < NT; ++mt) {
+      run[mt].raise(s[mt], c);
+      sum[mt] = run[mt].weights(s[mt], c, w[mt]);
+    }
   }
-  u32x4 pf[NT][NQ];
 #pragma unroll
   for (int mt = 0; mt < NT; ++mt) {
-    float w[8];
-    run[mt].weights(s[mt], scale_log2, w);
-    weight_operand<BF16ROWS>(w, pf[mt]);
+    run[mt].l += sum[mt];
+    u32x4 pf[NQ];
+    weight_operand<BF16ROWS>(w[mt], pf);
+#pragma unroll
+    for (int d = 0; d < DV; ++d)
+#pragma unroll
+      for (int i = NQ - 1; i >= 0; --i) run[mt].acc[d] = mfma(vf[d], pf[i], run[mt].acc[d]);
   }
-#pragma unroll
-  for (int d = 0; d < DV; ++d)
-#pragma unroll
-    for (int mt = 0; mt < NT; ++mt)
-#pragma unroll
-      for (int i = NQ - 1; i >= 0; --i) run[mt].acc[d] = mfma(vf[d], pf[mt][i], run[mt].acc[d]);
 }
 
 // Steps [t0, t1) of a pair by a wave with NT 16-row tiles from row tile mt0 of the block on.  Waves of
