@@ -332,8 +332,9 @@ __device__ __forceinline__ unsigned clean_pair(unsigned x) {
 // A value that is not finite must not meet a column that does not see it (its weight there is 0,
 // and 0 * inf is NaN), so in the steps that hold new rows such values are left out of the products
 // (clean_pair).  Here, once and rarely, they are added to the columns that do see them: positions
-// [from, to) of the request, sums of channels DV (4 g + i) + d.
-template <int D, bool FP8, int MT>
+// [from, to) of the request.  TILE: the tile kernel's sums acc[d][i] of channel 16 d + 4 g + i, else the
+// stream kernel's of channel DV (4 g + i) + d.
+template <int D, bool FP8, bool TILE, int MT>
 __device__ __forceinline__ void add_odd(const AttendParams &p, const Lens &len, const int32_t *tab, int h, int from,
                                         int to, const u64 (&see)[MT], Running<D / 16> (&run)[MT], int g) {
   constexpr int DV = D / 16;
@@ -347,7 +348,7 @@ __device__ __forceinline__ void add_odd(const AttendParams &p, const Lens &len, 
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int d = 0; d < DV; ++d) {
-        const size_t at = row * D + DV * (4 * g + i) + d;
+        const size_t at = row * D + (TILE ? 16 * d + 4 * g + i : DV * (4 * g + i) + d);
         float v = 0.f;  // e4m3 has no infinities, and its scales are finite
         if constexpr (FP8) v = (p.c.v[at] & 0x7fu) == 0x7fu ? __builtin_nanf("") : 0.f;
         else v = bf16_bits_to_f32(reinterpret_cast<const uint16_t *>(p.c.v)[at]);
@@ -530,7 +531,7 @@ __global__ __launch_bounds__(64 * kWaves, (stream_groups<D, BF16ROWS>())) void a
     if (__any(odd))
       for (int t = t0 + wave; t < t1; t += kWaves)
         if ((t + 1) * kStreamKeys > len.ctx)
-          add_odd<D, FP8, 1>(p, len, tab, h, t * kStreamKeys, min((t + 1) * kStreamKeys, total), q.see, run, g);
+          add_odd<D, FP8, false, 1>(p, len, tab, h, t * kStreamKeys, min((t + 1) * kStreamKeys, total), q.see, run, g);
 
     // the column's sum of weights over the lane groups, then the waves joined
     float l = run[0].l;
@@ -600,134 +601,128 @@ constexpr int kTileLeast = 4;  // tiles per workgroup
 constexpr int kTileGroups = 2;
 constexpr int tile_most(bool bf16_rows) { return bf16_rows ? 2 : 1; }
 
-// Where a lane's 16 bytes lie within the 16 of its group, so that the 8 consecutive lanes of a store,
-// which have two rows of four groups (keys) or four channels of two products (values), hit 8 places
-// that differ mod 8, as the 8 consecutive lanes of a load do.
-__device__ __forceinline__ int swap_k(int r, int g) { return r ^ (2 * g); }
-__device__ __forceinline__ int swap_v(int c, int j) { return c ^ (j & 4); }
+// Where the 16-byte piece ch of a staged row r lies.  The pieces change places within their row, so
+// that neither 8 lanes that read one piece of 8 key rows nor 32 that read two pieces of 8 value rows
+// meet in a bank.
+template <int D>
+__device__ __forceinline__ int place(int r, int ch) {
+  return r * (D / 8) + (ch ^ ((2 * (r & 3) + 9 * ((r >> 3) & 1)) & (D / 8 - 1)));
+}
 
-// One workgroup's staging of a 64-key tile: what a thread holds between loading and storing it.
-// each of 256 (d = 128) or 128 threads has eight keys of four value channels, and each of 256 a quarter
-// of one key row (all its 16-byte chunks of one residue mod 4).
+// One workgroup's staging of a 64-key tile as bf16 rows of keys and of values; a wave has 16 rows of each.
+// bf16 caches go from memory to LDS without passing through registers, e4m3 ones are held in registers
+// until they are converted and stored (a thread has a quarter of a row).
 template <int D, bool FP8>
 struct Stage {
-  static constexpr int KS = D / 32, DV = D / 16;
-  static constexpr int VC = D / 4;                       // threads per 8 keys of values
-  static constexpr int JV = 8 * VC;                      // value threads
-  static constexpr int KC = FP8 ? D / 64 : D / 32;       // 16-byte loads per key thread
-  u32x2 v[8];                                            // four channels of eight keys (e4m3: first half)
-  u32x4 k[KC];
-  u64 vsc;
-  unsigned ksc;
-  int pgv, pgk;                                          // page ids of the tile to be loaded next
-  bool has_v;
-  int kg, cc, row, quarter;
+  static constexpr int CH = D / 8;                       // 16-byte pieces of a bf16 row
+  static constexpr int RP = 64 / CH;                     // rows per load of a wave
+  static constexpr int KC = FP8 ? D / 64 : 1;            // 16-byte loads per thread
+  u32x4 k[KC], v[KC];
+  unsigned ksc, vsc;
+  int page;                                              // of the tile to be loaded next
+  int wave, lane;
 
-  __device__ __forceinline__ void init(int tid) {
-    has_v = tid < JV;
-    kg = (tid / VC) & 7;
-    cc = tid % VC;
-    row = tid >> 2;
-    quarter = tid & 3;
-  }
-  // Positions past the last row are loaded as rows of the last group or as the last row (and masked),
-  // pages out of range as page 0 (and the result becomes NaN): every load is in bounds.  The ids are
-  // loaded a tile before they are looked at, so that nothing waits for them.
-  __device__ __forceinline__ int group(int pos0, int total) const { return min(pos0 + 8 * kg, (total - 1) & ~7); }
+  __device__ __forceinline__ int row() const { return 16 * wave + (lane >> 2); }
+  // Positions past the last row are loaded as the last row (and masked), pages out of range as page 0
+  // (and the result becomes NaN): every load is in bounds.  The ids are loaded a tile before they are
+  // looked at, so that nothing waits for them.
   __device__ __forceinline__ void pages(const AttendParams &p, const int32_t *tab, int pos0, int total) {
-    pgv = tab[group(pos0, total) >> p.c.shift];
-    pgk = tab[min(pos0 + row, total - 1) >> p.c.shift];
+    page = tab[min(pos0 + (FP8 ? row() : 16 * wave), total - 1) >> p.c.shift];
   }
-  __device__ __forceinline__ void load(const AttendParams &p, int h, int pos0, int total, bool &bad) {
-    if ((unsigned)pgv >= (unsigned)p.c.pages) { bad = true; pgv = 0; }
-    if ((unsigned)pgk >= (unsigned)p.c.pages) { bad = true; pgk = 0; }
-    const size_t rk = p.c.row(pgk, h, min(pos0 + row, total - 1));
-    const unsigned char *src = p.c.k + rk * (FP8 ? D : 2 * D) + 16 * quarter;
+  __device__ __forceinline__ void load(const AttendParams &p, u32x4 *sk, u32x4 *sv, int h, int pos0, int total, bool &bad) {
+    if constexpr (FP8) {
+      if ((unsigned)page >= (unsigned)p.c.pages) { bad = true; page = 0; }
+      const size_t r = p.c.row(page, h, min(pos0 + row(), total - 1));
+      const size_t at = r * D + 16 * (lane & 3);
 #pragma unroll
-    for (int i = 0; i < KC; ++i) k[i] = *reinterpret_cast<const u32x4 *>(src + 64 * i);
-    if constexpr (FP8) ksc = p.c.ks[rk];
-    if (JV == 256 || has_v) {
-      const int at = group(pos0, total);
-      const size_t rv = p.c.row(pgv, h, at);
-      const unsigned char *vs = p.c.v + rv * (FP8 ? D : 2 * D) + (FP8 ? 4 : 8) * cc;
-      const int last = total - 1 - at;
-      const auto one = [&](int e, int from) {
-        if constexpr (FP8) v[e][0] = *reinterpret_cast<const unsigned *>(vs + from * D);
-        else v[e] = *reinterpret_cast<const u32x2 *>(vs + from * (2 * D));
-      };
-      if (pos0 + kTileKeys <= total) {  // constant offsets
-#pragma unroll
-        for (int e = 0; e < 8; ++e) one(e, e);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) one(e, min(e, last));
+      for (int i = 0; i < KC; ++i) {
+        k[i] = *reinterpret_cast<const u32x4 *>(p.c.k + at + 64 * i);
+        v[i] = *reinterpret_cast<const u32x4 *>(p.c.v + at + 64 * i);
       }
-      if constexpr (FP8) vsc = *reinterpret_cast<const u64 *>(p.c.vs + rv);
+      ksc = p.c.ks[r];
+      vsc = p.c.vs[r];
+    } else {
+      // a wave's 16 rows are of one page, those past the last row of the last row's
+      int pg = uniform(page);
+      if ((unsigned)pg >= (unsigned)p.c.pages) { bad = true; pg = 0; }
+      const int from = pos0 + 16 * wave, last = total - 1;
+      const size_t r0 = p.c.row(pg, h, min(from, last));
+      const unsigned char *k0 = p.c.k + r0 * (2 * D), *v0 = p.c.v + r0 * (2 * D);
+#pragma unroll
+      for (int i = 0; i < 16 / RP; ++i) {
+        const int r = RP * i + lane / CH;
+        const int off = min(r, max(last - from, 0)) * (2 * D) + 16 * (place<D>(r, lane % CH) % CH);
+        to_lds(k0 + off, sk + (16 * wave + RP * i) * CH);
+        to_lds(v0 + off, sv + (16 * wave + RP * i) * CH);
+      }
     }
   }
-  // Stores the loaded tile as operands: keys [32-key half][product][channel step][lane], values
-  // [half][product][lane], 16 bytes each.  masked: the tile holds new rows.
-  __device__ __forceinline__ void store(u32x4 *sk, u32x4 *sv, int pos0, int total, bool masked, bool &odd) const {
-    if (JV == 256 || has_v) {
-      u32x2 x[8];
-      const int last = total - 1 - group(pos0, total);
+  // 16 bytes per lane, from each lane's address to consecutive places from dst on.
+  static __device__ __forceinline__ void to_lds(const unsigned char *src, u32x4 *dst) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
+                                     (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
+  }
+  // Completes the tile (before the barrier that hands it on).  masked: it holds new rows, whose values
+  // that are not finite are taken out.
+  __device__ __forceinline__ void finish(u32x4 *sk, u32x4 *sv, bool masked, bool &odd) {
+    if constexpr (FP8) {
+      const float a = scale_of(ksc), b = scale_of(vsc);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if constexpr (FP8) {
-          const float s = scale_of((unsigned)(vsc >> (8 * min(e, last))) & 255u);
-          x[e] = u32x2{fp8_pair<false>(v[e][0], s), fp8_pair<true>(v[e][0], s)};
-        } else {
-          x[e] = v[e];
+      for (int i = 0; i < KC; ++i)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const int at = place<D>(row(), 2 * ((lane & 3) + 4 * i) + hf);
+          sk[at] = u32x4{fp8_pair<false>(k[i][2 * hf], a), fp8_pair<true>(k[i][2 * hf], a),
+                         fp8_pair<false>(k[i][2 * hf + 1], a), fp8_pair<true>(k[i][2 * hf + 1], a)};
+          u32x4 y = {fp8_pair<false>(v[i][2 * hf], b), fp8_pair<true>(v[i][2 * hf], b),
+                     fp8_pair<false>(v[i][2 * hf + 1], b), fp8_pair<true>(v[i][2 * hf + 1], b)};
+          if (masked) y = clean(y, odd);
+          sv[at] = y;
         }
-      }
-      if (masked) {
+    } else {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      if (masked)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const unsigned a = rarely(x[e][0]), b = rarely(x[e][1]);
-          odd = odd || odd_bf16_pair(a) || odd_bf16_pair(b);
-          x[e] = u32x2{clean_pair(a), clean_pair(b)};
+        for (int i = 0; i < 16 / RP; ++i) {
+          u32x4 *at = sv + (16 * wave + RP * i) * CH + lane;
+          *at = clean(*at, odd);
         }
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        u32x4 y;
-#pragma unroll
-        for (int k2 = 0; k2 < 4; ++k2)
-          y[k2] = __builtin_amdgcn_perm(x[2 * k2 + 1][j >> 1], x[2 * k2][j >> 1], j & 1 ? 0x07060302u : 0x05040100u);
-        const int ch = 4 * cc + j;
-        sv[((kg >> 2) * DV + ch % DV) * 64 + (kg & 3) * 16 + swap_v(ch / DV, ch % DV)] = y;
-      }
     }
-    const int at = ((row >> 5) * 2 + ((row >> 2) & 1)) * KS, r = 4 * ((row & 31) >> 3) + (row & 3);
+  }
+  static __device__ __forceinline__ u32x4 clean(u32x4 y, bool &odd) {
 #pragma unroll
-    for (int i = 0; i < KC; ++i) {
-      if constexpr (FP8) {
-        const float s = scale_of(ksc);
-        const int q = quarter + 4 * i;  // channels 16 q .. 16 q + 15
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf)
-          sk[(at + (q >> 1)) * 64 + (2 * (q & 1) + hf) * 16 + swap_k(r, 2 * (q & 1) + hf)] =
-              u32x4{fp8_pair<false>(k[i][2 * hf], s), fp8_pair<true>(k[i][2 * hf], s),
-                    fp8_pair<false>(k[i][2 * hf + 1], s), fp8_pair<true>(k[i][2 * hf + 1], s)};
-      } else {
-        sk[(at + i) * 64 + quarter * 16 + swap_k(r, quarter)] = k[i];
-      }
+    for (int e = 0; e < 4; ++e) {
+      const unsigned x = rarely(y[e]);
+      odd = odd || odd_bf16_pair(x);
+      y[e] = clean_pair(x);
     }
+    return y;
   }
 };
 
+// Eight keys' values of one channel as an operand: two reads of four rows that come transposed, a row's
+// 16 channels from four lanes of 8 bytes each.
+__device__ __forceinline__ u32x4 read_values(const unsigned char *at, int rows4) {
+  typedef short s16x4 __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) s16x4 *lds;
+  const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(at)));
+  const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(at + rows4)));
+  return u32x4{a[0], a[1], b[0], b[1]};
+}
+
 // One 32-key half of a staged tile for a wave's NT 16-row tiles.
 template <int D, bool BF16ROWS, int NT>
-__device__ __forceinline__ void tile_half(const u32x4 *sk, const u32x4 *sv, const Queries<D, BF16ROWS, NT> &q,
+__device__ __forceinline__ void tile_half(u32x4 *sk, u32x4 *sv, const Queries<D, BF16ROWS, NT> &q,
                                           Running<D / 16> (&run)[NT], float scale_log2, int lane, int slot0) {
   constexpr int KS = D / 32, DV = D / 16, NQ = BF16ROWS ? 1 : 3;
-  const int g = lane >> 4;
+  const int c = lane & 15, g = lane >> 4;
   f32x4 s[NT][2];
 #pragma unroll
   for (int mt = 0; mt < NT; ++mt) s[mt][0] = s[mt][1] = f32x4{0.f, 0.f, 0.f, 0.f};
   u32x4 kf[2 * KS], vf[DV];
 #pragma unroll
-  for (int i = 0; i < 2 * KS; ++i) kf[i] = sk[i * 64 + 16 * g + swap_k(lane & 15, g)];
+  for (int i = 0; i < 2 * KS; ++i)  // keys 8 (c / 4) + 4 hh + c % 4
+    kf[i] = sk[place<D>(8 * (c >> 2) + (c & 3), 4 * (i % KS) + g) + 4 * (i / KS) * (D / 8)];
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int ks = 0; ks < KS; ++ks)
@@ -739,7 +734,8 @@ __device__ __forceinline__ void tile_half(const u32x4 *sk, const u32x4 *sv, cons
         for (int i = NQ - 1; i >= 0; --i) s[mt][hh] = mfma(kf[hh * KS + ks], q.f[mt][ks][i], s[mt][hh]);
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-  for (int d = 0; d < DV; ++d) vf[d] = sv[d * 64 + 16 * g + swap_v(lane & 15, d)];
+  for (int d = 0; d < DV; ++d)  // keys 8 g + (0 .. 7), channel 16 d + c
+    vf[d] = read_values(reinterpret_cast<unsigned char *>(sv + place<D>(8 * g + (c >> 2), 2 * d + ((c >> 1) & 1))) + 8 * (c & 1), 8 * D);
   __builtin_amdgcn_sched_barrier(0);
   if (slot0 + 32 > 0) {  // new rows, or positions past the last one
     const int from = rarely(slot0 + 8 * g);
@@ -777,9 +773,9 @@ __device__ __forceinline__ void tile_half(const u32x4 *sk, const u32x4 *sv, cons
 // one workgroup may differ in NT: they stage together and meet at the same barriers.
 template <int D, bool FP8, bool BF16ROWS, int NT>
 __device__ __forceinline__ void tile_pair(const AttendParams &p, const Part<D> &part, const Lens &len, Stage<D, FP8> &stage,
-                                          u32x4 *s_k, u32x4 *s_v, int b, int h, int first, int rows, int mt0, int t0,
-                                          int t1, bool whole, size_t slot, int lane) {
-  constexpr int DV = D / 16, KF = 2 * (D / 32) * 64, VF = DV * 64;  // 16-byte pieces of a 32-key half
+                                          u32x4 *k0, u32x4 *v0, u32x4 *k1, u32x4 *v1, int b, int h, int first, int rows,
+                                          int mt0, int t0, int t1, bool whole, size_t slot, int lane) {
+  constexpr int DV = D / 16;
   constexpr int N1 = NT > 0 ? NT : 1;
   const int c = lane & 15, g = lane >> 4, Hq = p.c.H * p.G, total = len.ctx + len.n;
   Queries<D, BF16ROWS, N1> q;
@@ -793,30 +789,35 @@ __device__ __forceinline__ void tile_pair(const AttendParams &p, const Part<D> &
   if (!len.bad) {
     const int32_t *tab = p.c.table + (size_t)b * p.c.max_pages;
     stage.pages(p, tab, t0 * kTileKeys, total);
-    stage.load(p, h, t0 * kTileKeys, total, bad);
+    stage.load(p, k0, v0, h, t0 * kTileKeys, total, bad);
     if (t0 + 1 < t1) stage.pages(p, tab, (t0 + 1) * kTileKeys, total);
-    stage.store(s_k, s_v, t0 * kTileKeys, total, (t0 + 1) * kTileKeys > len.ctx, odd);
+    stage.finish(k0, v0, (t0 + 1) * kTileKeys > len.ctx, odd);
     __syncthreads();
-    for (int t = t0; t < t1; ++t) {
-      const int buf = (t - t0) & 1, pos0 = t * kTileKeys;
+    // The tile t is in k, v; the next one is brought to nk, nv meanwhile.
+    const auto one = [&](int t, u32x4 *k, u32x4 *v, u32x4 *nk, u32x4 *nv) {
+      const int pos0 = t * kTileKeys;
       if (t + 1 < t1) {
-        stage.load(p, h, pos0 + kTileKeys, total, bad);
+        stage.load(p, nk, nv, h, pos0 + kTileKeys, total, bad);
         if (t + 2 < t1) stage.pages(p, tab, pos0 + 2 * kTileKeys, total);
       }
       if constexpr (NT > 0)
+#pragma unroll 1
         for (int hf = 0; hf < 2; ++hf)
-          tile_half<D, BF16ROWS, NT>(s_k + (2 * buf + hf) * KF, s_v + (2 * buf + hf) * VF, q, run, p.scale_log2, lane,
+          tile_half<D, BF16ROWS, NT>(k + hf * 32 * (D / 8), v + hf * 32 * (D / 8), q, run, p.scale_log2, lane,
                                      pos0 + 32 * hf - len.ctx);
       if (t + 1 < t1) {
-        stage.store(s_k + 2 * (buf ^ 1) * KF, s_v + 2 * (buf ^ 1) * VF, pos0 + kTileKeys, total,
-                    pos0 + 2 * kTileKeys > len.ctx, odd);
+        stage.finish(nk, nv, pos0 + 2 * kTileKeys > len.ctx, odd);
         __syncthreads();
       }
+    };
+    for (int t = t0; t < t1; t += 2) {
+      one(t, k0, v0, k1, v1);
+      if (t + 1 < t1) one(t + 1, k1, v1, k0, v0);
     }
     odd = __syncthreads_or(odd);
     if constexpr (NT > 0)
       if (odd)
-        add_odd<D, FP8, NT>(p, len, tab, h, max(t0, len.ctx / kTileKeys) * kTileKeys, min(t1 * kTileKeys, total), q.see, run, g);
+        add_odd<D, FP8, true, NT>(p, len, tab, h, max(t0, len.ctx / kTileKeys) * kTileKeys, min(t1 * kTileKeys, total), q.see, run, g);
   }
   bad = __syncthreads_or(bad);  // and all waves are done with the last tile
   if constexpr (NT > 0) {
@@ -833,24 +834,20 @@ __device__ __forceinline__ void tile_pair(const AttendParams &p, const Part<D> &
         part.stat(slot, r)[1] = l;
       }
       const float inv = 1.f / l;
+      const size_t at = (((size_t)b * p.R + m / p.G) * Hq + (size_t)h * p.G + m % p.G) * D + 4 * g;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {  // channels DV (4 g + i) .. + DV - 1
-        float y[DV];
-#pragma unroll
-        for (int d = 0; d < DV; ++d) y[d] = whole ? run[mt].acc[d][i] * inv : run[mt].acc[d][i];
-        const int ch = DV * (4 * g + i);
-        const size_t at = (((size_t)b * p.R + m / p.G) * Hq + (size_t)h * p.G + m % p.G) * D + ch;
-        if (whole && BF16ROWS) {
-          uint16_t *dst = static_cast<uint16_t *>(p.o) + at;
-          if constexpr (DV == 8)
-            *reinterpret_cast<u32x4 *>(dst) = u32x4{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7])};
-          else
-            *reinterpret_cast<u32x2 *>(dst) = u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
-        } else {
-          float *dst = whole ? static_cast<float *>(p.o) + at : part.sums(slot, r) + ch;
-#pragma unroll
-          for (int d = 0; d < DV; d += 4) *reinterpret_cast<f32x4 *>(dst + d) = f32x4{y[d], y[d + 1], y[d + 2], y[d + 3]};
+      for (int d = 0; d < DV; ++d) {  // channels 16 d + 4 g .. + 3
+        f32x4 y = run[mt].acc[d];
+        if (!whole) {
+          *reinterpret_cast<f32x4 *>(part.sums(slot, r) + 16 * d + 4 * g) = y;
+          continue;
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] *= inv;
+        if constexpr (BF16ROWS)
+          *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(p.o) + at + 16 * d) = u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+        else
+          *reinterpret_cast<f32x4 *>(static_cast<float *>(p.o) + at + 16 * d) = y;
       }
     }
   }
@@ -858,11 +855,13 @@ __device__ __forceinline__ void tile_pair(const AttendParams &p, const Part<D> &
 
 template <int D, bool FP8, bool BF16ROWS, int MT>
 __global__ __launch_bounds__(64 * kWaves, kTileGroups) void attend_tile_kernel(AttendParams p, Cut cut) {
-  __shared__ u32x4 s_k[4 * 2 * (D / 32) * 64], s_v[4 * (D / 16) * 64];  // two tiles of two halves
+  constexpr int TILE = kTileKeys * (D / 8);  // two tiles, in arrays of their own: reads of one do not wait for loads of the other
+  __shared__ u32x4 s_k0[TILE], s_v0[TILE], s_k1[TILE], s_v1[TILE];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const Part<D> part{p.part, cut};
   Stage<D, FP8> stage;
-  stage.init(tid);
+  stage.wave = wave;
+  stage.lane = lane;
   Walk walk(p, cut, lane);
   Seg sg;
   int t0, t1;
@@ -877,11 +876,11 @@ __global__ __launch_bounds__(64 * kWaves, kTileGroups) void attend_tile_kernel(A
     const bool whole = t0 == 0 && t1 == sg.steps;
     const size_t slot = part.slot(walk.rb, walk.w, t0 == 0);
     if (MT > 1 && nt == 2)
-      tile_pair<D, FP8, BF16ROWS, MT>(p, part, len, stage, s_k, s_v, sg.b, sg.h, first, rows, mt0, t0, t1, whole, slot, lane);
+      tile_pair<D, FP8, BF16ROWS, MT>(p, part, len, stage, s_k0, s_v0, s_k1, s_v1, sg.b, sg.h, first, rows, mt0, t0, t1, whole, slot, lane);
     else if (nt == 1)
-      tile_pair<D, FP8, BF16ROWS, 1>(p, part, len, stage, s_k, s_v, sg.b, sg.h, first, rows, mt0, t0, t1, whole, slot, lane);
+      tile_pair<D, FP8, BF16ROWS, 1>(p, part, len, stage, s_k0, s_v0, s_k1, s_v1, sg.b, sg.h, first, rows, mt0, t0, t1, whole, slot, lane);
     else
-      tile_pair<D, FP8, BF16ROWS, 0>(p, part, len, stage, s_k, s_v, sg.b, sg.h, first, rows, mt0, t0, t1, whole, slot, lane);
+      tile_pair<D, FP8, BF16ROWS, 0>(p, part, len, stage, s_k0, s_v0, s_k1, s_v1, sg.b, sg.h, first, rows, mt0, t0, t1, whole, slot, lane);
   }
 }
 
