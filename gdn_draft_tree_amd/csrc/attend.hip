@@ -632,8 +632,9 @@ struct Stage {
   __device__ __forceinline__ void load(const AttendParams &p, u32x4 *sk, u32x4 *sv, int h, int pos0, int total, bool &bad) {
     if constexpr (FP8) {
       if ((unsigned)page >= (unsigned)p.c.pages) { bad = true; page = 0; }
-      const size_t r = p.c.row(page, h, min(pos0 + row(), total - 1));
-      const size_t at = r * D + 16 * (lane & 3);
+      const int l = rarely(lane);
+      const size_t r = p.c.row(page, h, min(pos0 + 16 * wave + (l >> 2), total - 1));
+      const size_t at = r * D + 16 * (l & 3);
 #pragma unroll
       for (int i = 0; i < KC; ++i) {
         k[i] = *reinterpret_cast<const u32x4 *>(p.c.k + at + 64 * i);
@@ -667,11 +668,12 @@ struct Stage {
   __device__ __forceinline__ void finish(u32x4 *sk, u32x4 *sv, bool masked, bool &odd) {
     if constexpr (FP8) {
       const float a = scale_of(ksc), b = scale_of(vsc);
+      const int l = rarely(lane);  // the places are computed anew: registers are scarcer than time
 #pragma unroll
       for (int i = 0; i < KC; ++i)
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          const int at = place<D>(row(), 2 * ((lane & 3) + 4 * i) + hf);
+          const int at = place<D>(16 * wave + (l >> 2), 2 * ((l & 3) + 4 * i) + hf);
           sk[at] = u32x4{fp8_pair<false>(k[i][2 * hf], a), fp8_pair<true>(k[i][2 * hf], a),
                          fp8_pair<false>(k[i][2 * hf + 1], a), fp8_pair<true>(k[i][2 * hf + 1], a)};
           u32x4 y = {fp8_pair<false>(v[i][2 * hf], b), fp8_pair<true>(v[i][2 * hf], b),
@@ -710,20 +712,27 @@ __device__ __forceinline__ u32x4 read_values(const unsigned char *at, int rows4)
   return u32x4{a[0], a[1], b[0], b[1]};
 }
 
-// One 32-key half of a staged tile for a wave's NT 16-row tiles.
-template <int D, bool BF16ROWS, int NT>
-__device__ __forceinline__ void tile_half(u32x4 *sk, u32x4 *sv, const Queries<D, BF16ROWS, NT> &q,
-                                          Running<D / 16> (&run)[NT], float scale_log2, int lane, int slot0) {
+// The keys of a 32-key half as operands: keys 8 (c / 4) + 4 hh + c % 4, then the same of four keys on.
+template <int D>
+__device__ __forceinline__ void read_keys(const u32x4 *sk, u32x4 (&kf)[D / 16], int lane) {
+  constexpr int KS = D / 32;
+  const int c = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int i = 0; i < 2 * KS; ++i) kf[i] = sk[place<D>(8 * (c >> 2) + (c & 3), 4 * (i % KS) + g) + 4 * (i / KS) * (D / 8)];
+}
+
+// One 32-key half of a staged tile, whose keys are in kf, for a wave's NT 16-row tiles.  `early` runs
+// when the keys' registers are free, `late` when nothing of the half is left in LDS: there the next
+// keys are read, so that the next half's first product does not wait for them.
+template <int D, bool BF16ROWS, int NT, class Early, class Late>
+__device__ __forceinline__ void tile_half(const u32x4 (&kf)[D / 16], u32x4 *sv, const Queries<D, BF16ROWS, NT> &q,
+                                          Running<D / 16> (&run)[NT], float scale_log2, int lane, int slot0,
+                                          const Early &early, const Late &late) {
   constexpr int KS = D / 32, DV = D / 16, NQ = BF16ROWS ? 1 : 3;
   const int c = lane & 15, g = lane >> 4;
   f32x4 s[NT][2];
 #pragma unroll
   for (int mt = 0; mt < NT; ++mt) s[mt][0] = s[mt][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-  u32x4 kf[2 * KS], vf[DV];
-#pragma unroll
-  for (int i = 0; i < 2 * KS; ++i)  // keys 8 (c / 4) + 4 hh + c % 4
-    kf[i] = sk[place<D>(8 * (c >> 2) + (c & 3), 4 * (i % KS) + g) + 4 * (i / KS) * (D / 8)];
-  __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
@@ -733,9 +742,11 @@ __device__ __forceinline__ void tile_half(u32x4 *sk, u32x4 *sv, const Queries<D,
 #pragma unroll
         for (int i = NQ - 1; i >= 0; --i) s[mt][hh] = mfma(kf[hh * KS + ks], q.f[mt][ks][i], s[mt][hh]);
   __builtin_amdgcn_sched_barrier(0);
+  u32x4 vf[DV];
 #pragma unroll
   for (int d = 0; d < DV; ++d)  // keys 8 g + (0 .. 7), channel 16 d + c
     vf[d] = read_values(reinterpret_cast<unsigned char *>(sv + place<D>(8 * g + (c >> 2), 2 * d + ((c >> 1) & 1))) + 8 * (c & 1), 8 * D);
+  early();
   __builtin_amdgcn_sched_barrier(0);
   if (slot0 + 32 > 0) {  // new rows, or positions past the last one
     const int from = rarely(slot0 + 8 * g);
@@ -750,23 +761,27 @@ __device__ __forceinline__ void tile_half(u32x4 *sk, u32x4 *sv, const Queries<D,
     ok = ok && Running<DV>::fits(sum[mt]);
   }
   if (__any(!ok)) {
-    const float c = rarely(scale_log2);
+    const float c2 = rarely(scale_log2);
 #pragma unroll
     for (int mt = 0; mt < NT; ++mt) {
-      run[mt].raise(s[mt], c);
-      sum[mt] = run[mt].weights(s[mt], c, w[mt]);
+      run[mt].raise(s[mt], c2);
+      sum[mt] = run[mt].weights(s[mt], c2, w[mt]);
     }
   }
+  u32x4 pf[NT][NQ];
 #pragma unroll
   for (int mt = 0; mt < NT; ++mt) {
     run[mt].l += sum[mt];
-    u32x4 pf[NQ];
-    weight_operand<BF16ROWS>(w[mt], pf);
+    weight_operand<BF16ROWS>(w[mt], pf[mt]);
+  }
+  late();
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int mt = 0; mt < NT; ++mt)
 #pragma unroll
     for (int d = 0; d < DV; ++d)
 #pragma unroll
-      for (int i = NQ - 1; i >= 0; --i) run[mt].acc[d] = mfma(vf[d], pf[i], run[mt].acc[d]);
-  }
+      for (int i = NQ - 1; i >= 0; --i) run[mt].acc[d] = mfma(vf[d], pf[mt][i], run[mt].acc[d]);
 }
 
 // Steps [t0, t1) of a pair by a wave with NT 16-row tiles from row tile mt0 of the block on.  Waves of
@@ -793,21 +808,31 @@ __device__ __forceinline__ void tile_pair(const AttendParams &p, const Part<D> &
     if (t0 + 1 < t1) stage.pages(p, tab, (t0 + 1) * kTileKeys, total);
     stage.finish(k0, v0, (t0 + 1) * kTileKeys > len.ctx, odd);
     __syncthreads();
-    // The tile t is in k, v; the next one is brought to nk, nv meanwhile.
+    // The keys of a half are read during the half before, those of a tile's first half right after the
+    // barrier that hands it on: the values' product of the last half runs meanwhile (139 us against 157
+    // for 32 trees of 65 rows).
+    [[maybe_unused]] u32x4 kf[D / 16];
+    if constexpr (NT > 0) read_keys<D>(k0, kf, lane);
+    // The tile t is in k, v (its first keys in kf); the next one is brought to nk, nv meanwhile.
     const auto one = [&](int t, u32x4 *k, u32x4 *v, u32x4 *nk, u32x4 *nv) {
       const int pos0 = t * kTileKeys;
       if (t + 1 < t1) {
         stage.load(p, nk, nv, h, pos0 + kTileKeys, total, bad);
         if (t + 2 < t1) stage.pages(p, tab, pos0 + 2 * kTileKeys, total);
       }
-      if constexpr (NT > 0)
-#pragma unroll 1
-        for (int hf = 0; hf < 2; ++hf)
-          tile_half<D, BF16ROWS, NT>(k + hf * 32 * (D / 8), v + hf * 32 * (D / 8), q, run, p.scale_log2, lane,
-                                     pos0 + 32 * hf - len.ctx);
-      if (t + 1 < t1) {
-        stage.finish(nk, nv, pos0 + 2 * kTileKeys > len.ctx, odd);
-        __syncthreads();
+      const auto hand_on = [&] {
+        if (t + 1 < t1) {
+          stage.finish(nk, nv, pos0 + 2 * kTileKeys > len.ctx, odd);
+          __syncthreads();
+          if constexpr (NT > 0) read_keys<D>(nk, kf, lane);
+        }
+      };
+      if constexpr (NT > 0) {
+        tile_half<D, BF16ROWS, NT>(kf, v, q, run, p.scale_log2, lane, pos0 - len.ctx,
+                                   [&] { read_keys<D>(k + 32 * (D / 8), kf, lane); }, [] {});
+        tile_half<D, BF16ROWS, NT>(kf, v + 32 * (D / 8), q, run, p.scale_log2, lane, pos0 + 32 - len.ctx, [] {}, hand_on);
+      } else {
+        hand_on();
       }
     };
     for (int t = t0; t < t1; t += 2) {
