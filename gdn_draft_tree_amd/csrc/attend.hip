@@ -15,9 +15,7 @@
 //    such an order (row r of product h holds key 8 (r / 4) + 4 h + r % 4) that a lane ends up with
 //    the scores of the 8 consecutive keys 8 g .. 8 g + 7 of query c,
 //  * which is the operand layout the second product needs: O^T (channels x queries) = V^T P^T over
-//    the 32 keys.  Product j has channel c d / 16 + j in row c: a lane reads, for each of its keys,
-//    consecutive channels (whole rows, coalesced), and interleaves the keys' 16-bit halves in
-//    registers (v_perm).
+//    the 32 keys.
 // The softmax is thus per lane except for the maximum, and that is only joined across lanes when a
 // score exceeds the running one by far: until then the old maximum serves.
 //
@@ -25,9 +23,16 @@
 //  * at most 16 (a new token of up to 16 heads a group): the cache's bytes are all there is.
 //    attend_stream_kernel: every wave takes 32-key steps of its own, straight from global memory
 //    to operand registers, no LDS and no barrier until the waves join at the end.
+//    Product j of the values has channel c d / 16 + j in row c: a lane reads, for each of its keys,
+//    consecutive channels (whole rows, coalesced), and interleaves the keys' 16-bit halves in
+//    registers (v_perm).  Bound by HBM: one row of 8 x 8 heads over 131,000 positions (537 MB) 88.5 us,
+//    6.1 TB/s; 32 ragged contexts over e4m3 (562 MB) 102 us, 5.5 TB/s.
 //  * more (trees, chains): attend_tile_kernel: the four waves of a workgroup have up to two 16-row
-//    tiles each and share 64-key tiles of keys and values, which all of them stage in LDS in
-//    operand order (values already transposed, e4m3 already bf16), one tile ahead.
+//    tiles each and share 64-key tiles of keys and values, staged in LDS as bf16 rows one tile ahead
+//    (bf16 caches straight from memory, e4m3 converted on the way); the values' operands come out of
+//    LDS transposed (ds_read_b64_tr_b16).  Bound by the chain product - softmax - product of the two
+//    waves a SIMD has room for: 64 rows of 4 x 8 heads over 4,032 positions, 32 requests, 160 us,
+//    850 TFLOP/s (a large library product of this card: 1265); 32 trees of 65 rows 139 us.
 //
 // Work is cut by steps, not by requests: the steps of all (key-value head, request) pairs form one
 // list, and each of W workgroups (as many as are resident at once) takes an equal, contiguous part
@@ -36,7 +41,7 @@
 // any lengths.
 //
 // Arithmetic.  bf16 rows: the products of bf16 numbers are exact, accumulated in fp32; the weights
-// are rounded to bf16 for the second product (half a step, 2^-9 of a weight, against an output
+// are rounded to bf16 for the second product (half a step, 2^-8 of a weight, against an output
 // that is rounded to bf16 itself), their sum is of the fp32 weights.  fp32 rows: q and the weights
 // are split into three bf16 parts that hold their 24 bits, so every product is exact to fp32.
 // e4m3 cache rows become bf16 with their power-of-two scale in the conversion, exactly.
@@ -370,7 +375,10 @@ __device__ __forceinline__ void store_o(void *o, size_t e, float x) {
 
 constexpr int kWaves = 4;
 constexpr int kStreamKeys = 32;
-constexpr int kStreamLeast = 8;  // steps per workgroup: two per wave
+// Steps per workgroup at least, four per wave: fewer parts to join.  One row of 8 x 8 heads, in all: over 2,000
+// positions 22.9 us (19.0 with 8 steps, 31 with 32), over 16,000 28.0 (30.9, 36), four such requests over
+// 4,000 25.3 (29.1, 34).
+constexpr int kStreamLeast = 16;
 
 // Workgroups resident per CU (by registers): the width of the cut.
 template <int D, bool BF16ROWS>
@@ -592,7 +600,9 @@ __global__ __launch_bounds__(64 * kWaves, (stream_groups<D, BF16ROWS>())) void a
 // ---- more query rows -----------------------------------------------------------------------------
 
 constexpr int kTileKeys = 64;
-constexpr int kTileLeast = 4;  // tiles per workgroup
+// Tiles per workgroup at least: one tree of 65 rows of 4 x 8 heads over 4,000 positions 31 us (35 with 4, 38 with
+// 16), over 1,000 33 (30, 42), four trees of 25 rows over 4,000 40 (46, 46).
+constexpr int kTileLeast = 8;
 
 // Four waves of up to MT 16-row tiles each, two workgroups a CU: 256 registers, of which a tile's sums
 // take 32 and its queries 16 (48 split), so two tiles fit beside what is in flight (split: one).  (One workgroup a CU with
@@ -911,15 +921,22 @@ __global__ __launch_bounds__(64 * kWaves, kTileGroups) void attend_tile_kernel(A
 
 // ---- the join ------------------------------------------------------------------------------------
 
+// Rows are dealt out over kJoinShares workgroups of kJoinLanes lanes per cut (for 32 trees of 65 rows 14 us,
+// with one workgroup of 1024 lanes 15; for one such tree over 4,000 positions 34 us in all, and 39).
+constexpr int kJoinLanes = 256, kJoinShares = 4;
+// A row's parts from which on a workgroup takes its rows one after the other with all lanes, for each
+// such row (one row of 8 heads over 2,000 positions: 20 us in all, 23 where more than 2 parts do).
+constexpr int kTeamParts = 8;
+
 // Joins the partial results of every pair that a cut goes through: workgroup (w, row block) looks at
-// the cut behind part w, and the first cut of a pair has it.  Sums of few parts: 32 (d = 128) or 16
-// lanes per row, the parts in order.  Of many (a long context's few rows): all lane groups of a
-// workgroup on one row at a time, the parts dealt out over them.  TH: many rows (tile kernel) are
-// joined by 1024 lanes in one workgroup, the few of the stream kernel by 256 in each of up to four.
-template <int D, bool BF16ROWS, int TH>
-__global__ __launch_bounds__(TH) void attend_join_kernel(AttendParams p, Cut cut) {
+// the cut behind part w, and the first cut of a pair has it.  D / 4 lanes have a row, four of its parts
+// at a time and in order, the next four in flight meanwhile; of very many parts (a long context's few
+// rows) all lane groups of a workgroup take one row, the parts dealt out over them.
+template <int D, bool BF16ROWS>
+__global__ __launch_bounds__(kJoinLanes) void attend_join_kernel(AttendParams p, Cut cut) {
+  constexpr int TH = kJoinLanes;
   constexpr int LG = D / 4, GR = TH / LG;  // lanes per row, lane groups
-  constexpr int kFew = 4;
+  constexpr int kStep = 4;
   __shared__ float s_sum[GR][D], s_l[GR], s_top[TH / 64];
   const int tid = threadIdx.x, lane = tid & 63, grp = tid / LG, e = tid % LG;
   const int w0 = blockIdx.x, rb = blockIdx.y;
@@ -927,7 +944,7 @@ __global__ __launch_bounds__(TH) void attend_join_kernel(AttendParams p, Cut cut
   const long long x = (w0 + 1) * share;
   const Seg sg = locate(p, cut.keys, per, x, lane);
   if (sg.b < 0 || sg.off == 0 || sg.off > share) return;  // a pair starts here, or its first cut is another
-  const int last = (int)((x - sg.off + sg.steps - 1) / share), parts = last - w0 + 1;
+  const int last = (int)((x - sg.off + sg.steps - 1) / share), parts = uniform(last - w0 + 1);
   const Lens len = lens_of(p, sg.b);
   const int first = rb * cut.BM, rows = min(cut.BM, len.n * p.G - first), Hq = p.c.H * p.G;
   const Part<D> part{p.part, cut};
@@ -937,28 +954,47 @@ __global__ __launch_bounds__(TH) void attend_join_kernel(AttendParams p, Cut cut
     const int m = first + r;
     return (((size_t)sg.b * p.R + m / p.G) * Hq + (size_t)sg.h * p.G + m % p.G) * D;
   };
-  if (parts <= kFew) {
+  const int rounds = (rows + (int)gridDim.z - 1) / (int)gridDim.z;
+  if (parts <= kTeamParts * rounds) {
+    struct Four {
+      float st[kStep], sl[kStep];
+      f32x4 sum[kStep];
+    };
     for (int r = blockIdx.z * GR + grp; r < rows; r += gridDim.z * GR) {
-      float st[kFew], sl[kFew], top = kNegInf, l = 0.f;
-      f32x4 sum[kFew], o = {0.f, 0.f, 0.f, 0.f};
+      const auto load = [&](int i0) {
+        Four f;
 #pragma unroll
-      for (int i = 0; i < kFew; ++i)
-        if (i < parts) {
-          const size_t at = slot(i);
-          st[i] = part.stat(at, r)[0];
-          sl[i] = part.stat(at, r)[1];
-          sum[i] = *reinterpret_cast<const f32x4 *>(part.sums(at, r) + 4 * e);
-        }
+        for (int j = 0; j < kStep; ++j)
+          if (i0 + j < parts) {
+            const size_t at = slot(i0 + j);
+            f.st[j] = part.stat(at, r)[0];
+            f.sl[j] = part.stat(at, r)[1];
+            f.sum[j] = *reinterpret_cast<const f32x4 *>(part.sums(at, r) + 4 * e);
+          }
+        return f;
+      };
+      float top = kNegInf, l = 0.f;
+      f32x4 o = {0.f, 0.f, 0.f, 0.f};
+      Four next = load(0);
+      for (int i0 = 0; i0 < parts; i0 += kStep) {
+        const Four now = next;
+        if (i0 + kStep < parts) next = load(i0 + kStep);
+        float m = top;
 #pragma unroll
-      for (int i = 0; i < kFew; ++i)
-        if (i < parts) top = fmaxf(top, st[i]);
+        for (int j = 0; j < kStep; ++j)
+          if (i0 + j < parts) m = fmaxf(m, now.st[j]);
+        const float keep = top == m ? 1.f : __builtin_amdgcn_exp2f(top - m);
+        l *= keep;
+        o *= keep;
 #pragma unroll
-      for (int i = 0; i < kFew; ++i)
-        if (i < parts) {
-          const float f = st[i] == top ? 1.f : __builtin_amdgcn_exp2f(st[i] - top);
-          l += f * sl[i];
-          o += f * sum[i];
-        }
+        for (int j = 0; j < kStep; ++j)
+          if (i0 + j < parts) {
+            const float f = now.st[j] == m ? 1.f : __builtin_amdgcn_exp2f(now.st[j] - m);
+            l += f * now.sl[j];
+            o += f * now.sum[j];
+          }
+        top = m;
+      }
 #pragma unroll
       for (int k = 0; k < 4; ++k) o[k] /= l;
       if constexpr (BF16ROWS)
@@ -1011,6 +1047,8 @@ struct Shape {
 
 Shape shape_of(int R, int G, int D, bool bf16_rows) {
   const int tiles = (R * G + 15) / 16;
+  // 16 query rows at most: the stream kernel (32 requests of 16 x 8 heads over 4,000 positions 99 us, the tile
+  // kernel 107; one such request 26 and 41)
   if (tiles == 1) return Shape{0, Cut{16, 1, kCUs * (D == 64 ? 4 : bf16_rows ? 3 : 2), kStreamKeys, kStreamLeast}};
   const int most = kWaves * tile_most(bf16_rows);
   // W: a multiple of 8, so that all workgroups (which come in rounds of 8) are resident at once
@@ -1018,7 +1056,9 @@ Shape shape_of(int R, int G, int D, bool bf16_rows) {
   return Shape{(each + kWaves - 1) / kWaves, Cut{16 * each, blocks, kCUs * kTileGroups / blocks / 8 * 8, kTileKeys, kTileLeast}};
 }
 
-// Contexts that cannot be longer than this many positions go to one workgroup each: nothing to join.
+// Contexts that cannot be longer than this many positions (by the table's width) go to one workgroup each:
+// nothing to join.  Whole and split, us: one row of 8 x 8 heads over 990 positions 16 and 20, over 1,980 26 and
+// 21 (32 such requests: 27 and 37, 48 and 56); 25 rows of 4 x 8 heads over 480 18 and 21, over 990 28 and 23.
 constexpr int kWholeStream = 1024, kWholeTile = 512;
 bool is_whole(const Shape &s, long long positions) { return positions <= (s.MT == 0 ? kWholeStream : kWholeTile); }
 
@@ -1037,12 +1077,9 @@ hipError_t launch_rows(AttendParams p, hipStream_t stream) {
   else if constexpr (BF16ROWS)
     hipLaunchKernelGGL((attend_tile_kernel<D, FP8, BF16ROWS, 2>), grid, block, 0, stream, p, cut);
   if (hipError_t e = hipGetLastError(); e != hipSuccess || p.whole) return e;
-  if (s.MT == 0)
-    hipLaunchKernelGGL((attend_join_kernel<D, BF16ROWS, 256>), dim3((unsigned)(cut.W - 1), 1, (unsigned)min(p.R * p.G, 4)),
-                       dim3(256), 0, stream, p, cut);
-  else
-    hipLaunchKernelGGL((attend_join_kernel<D, BF16ROWS, 1024>), dim3((unsigned)(cut.W - 1), (unsigned)cut.blocks),
-                       dim3(1024), 0, stream, p, cut);
+  hipLaunchKernelGGL((attend_join_kernel<D, BF16ROWS>),
+                     dim3((unsigned)(cut.W - 1), (unsigned)cut.blocks, (unsigned)min(p.R * p.G, kJoinShares)),
+                     dim3(kJoinLanes), 0, stream, p, cut);
   return hipGetLastError();
 }
 

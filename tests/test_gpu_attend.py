@@ -7,8 +7,8 @@ scale * sum |q k| a row meets):
     which costs one more rounding of 2^-24 (E + 6); the exponential itself 2^-22.  A weight is then
     off by that much of itself, and so is the normaliser: twice the sum of these, times A;
   * sums of T terms in fp32: 2^-24 T each for the output and the normaliser;
-  * bf16 rows: weights rounded to bf16 (2^-9 of each at most, half of the 2^-8 a step is) and the
-    output rounded once (2^-9 of it); counted as 2^-8 each;
+  * bf16 rows: weights rounded to bf16 (half a step, 2^-8 of each at most) and the output rounded once
+    (2^-8 of it);
   * fp32 rows: weights in three bf16 parts (2^-24), the output rounded to fp32 (2^-24)."""
 import numpy as np
 import pytest
@@ -135,6 +135,18 @@ def test_long_and_ragged_contexts(kind, rows_kind, R):
     o = torch.full_like(q, 7.0)
     call(g, kv, table, q, ctx, [R] * 4, anc, o=o)
     check(o, q, vals, ctx, [R] * 4, anc, rows_kind)
+
+
+@pytest.mark.parametrize("kind,rows_kind,R,Hq,H,d,ctx", [
+    ("bf16", "bf16", 65, 8, 2, 128, 2999), ("e4m3", "bf16", 33, 4, 2, 64, 1501), ("bf16", "f32", 25, 2, 1, 128, 4100),
+    ("bf16", "bf16", 16, 2, 2, 64, 9001), ("e4m3", "f32", 5, 3, 1, 128, 6007)])
+def test_one_request_over_a_long_context(kind, rows_kind, R, Hq, H, d, ctx):
+    """A single request's many rows, each joined from many parts."""
+    import gdn_draft_tree_amd as g
+    kv, table, vals, q, anc = setup(g, 1, R, Hq, H, d, 64, kind, rows_kind, [ctx], [R], "tree", R)
+    o = torch.full_like(q, 7.0)
+    call(g, kv, table, q, [ctx], [R], anc, o=o)
+    check(o, q, vals, [ctx], [R], anc, rows_kind)
 
 
 @pytest.mark.parametrize("rows_kind", ["bf16", "f32"])
