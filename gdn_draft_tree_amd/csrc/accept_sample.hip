@@ -560,7 +560,8 @@ size_t accept_sample_workspace(int B, int R, int V) {
 }
 
 bool sample_fits(int B, int R, int V) {
-  return (long long)B * R * stat_chunks((long long)B * R, V) < 0x7fffffffLL && (long long)B * sum_parts(V) < 0x7fffffffLL;
+  return (long long)B * R <= kMaxGroups && (long long)B * R * stat_chunks((long long)B * R, V) <= kMaxGroups &&
+         (long long)B * sum_parts(V) <= kMaxGroups;
 }
 
 hipError_t launch_accept_sample(const SampleParams &p, hipStream_t stream) {

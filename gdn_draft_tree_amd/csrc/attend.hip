@@ -1104,7 +1104,7 @@ size_t attend_workspace(int R, int G, int D, long long positions) {
 
 bool attend_fits(int B, int R, int G, int H) {
   // one workgroup per (request, head, row block) at most, in rounds of 8; 16 rows a block at least
-  return (long long)B * H + 8 < 0x7fffffffLL / ((R * G + 15) / 16);
+  return (long long)B * H + 8 < kMaxGroups / ((R * G + 15) / 16);
 }
 
 hipError_t launch_attend(const AttendParams &p, hipStream_t stream) {

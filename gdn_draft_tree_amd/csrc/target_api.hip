@@ -59,7 +59,8 @@ gdntree_status rows_call(const gdntree_cache &cache, int layer, const int32_t *t
   if (gdntree_status st = check_cache(cache, table, max_pages); st != GDNTREE_OK) return st;
   if (!start || !k || !v || !aligned(k) || !aligned(v)) return GDNTREE_ERR_ARG;
   if (layer < 0 || layer >= cache.L || B <= 0 || R <= 0 || !dtype_ok(dtype)) return GDNTREE_ERR_ARG;
-  if ((__int128)B * R * cache.H_kv > 0x7fffffffLL - 65536) return GDNTREE_ERR_UNSUPPORTED;  // rows, in 32 bits
+  // rows are counted in 32 bits, and a workgroup has 256 * 8 / d of them
+  if ((__int128)B * R * cache.H_kv * cache.d >= (__int128)kMaxGroups * 2048) return GDNTREE_ERR_UNSUPPORTED;
   if (gdntree_status st = device_ok(); st != GDNTREE_OK) return st;
   RowsParams p;
   p.c = view(cache, layer, table, max_pages);
@@ -100,8 +101,7 @@ GDNTREE_EXPORT gdntree_status gdntree_cache_commit(gdntree_cache cache, const in
   if (!ctx_len || !acc_len || !acc_node) return GDNTREE_ERR_ARG;
   if (B <= 0 || N <= 0 || P <= 0) return GDNTREE_ERR_ARG;
   if (N > kMaxN || P > kMaxP) return GDNTREE_ERR_UNSUPPORTED;
-  const __int128 blocks = (__int128)cache.L * B * cache.H_kv;
-  if (blocks >= 0x7fffffffLL) return GDNTREE_ERR_UNSUPPORTED;
+  if ((__int128)cache.L * B * ((cache.H_kv + 3LL) / 4) > kMaxGroups) return GDNTREE_ERR_UNSUPPORTED;
   if (gdntree_status st = device_ok(); st != GDNTREE_OK) return st;
   CacheCommitParams p;
   p.c = view(cache, 0, table, max_pages);

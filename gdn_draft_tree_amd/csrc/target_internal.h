@@ -11,6 +11,7 @@ constexpr int kMinPage = 16;   // positions of 8 consecutive keys share a page
 constexpr int kMaxPage = 256;
 constexpr int kMaxGroup = 16;  // query heads per key-value head
 constexpr int kMaxVocab = 1 << 24;
+constexpr long long kMaxGroups = 0xffffffffLL / 256;  // workgroups a launch: its work items are counted in 32 bits
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));

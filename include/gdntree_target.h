@@ -48,7 +48,9 @@ typedef enum { GDNTREE_CACHE_BF16 = 0, GDNTREE_CACHE_E4M3 = 1 } gdntree_cache_dt
  * 2^(byte - 127)).  A code times its scale is a bf16 number, so what is read back, by
  * gdntree_cache_read or by gdntree_attend, is exactly what was stored.
  *
- * Limits: page_size a power of two in [16, 256], d in {64, 128}; every pointer 16-byte aligned.
+ * Limits: page_size a power of two in [16, 256], d in {64, 128}; every pointer 16-byte aligned.  A call
+ * takes what one launch of 2^24 - 1 workgroups holds (written and read: B R H_kv d < 2^35); more is
+ * GDNTREE_ERR_UNSUPPORTED.
  * Requests may share pages that are only read (a common prefix); a page that is written by a
  * call must appear once in that call's table.
  */

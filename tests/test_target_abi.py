@@ -109,6 +109,17 @@ def test_accept_sample_refuses(kw, expect):
                                    *a["acc"], a["ws"], a["size"], None) == expect
 
 
+def test_more_than_a_launch_holds_is_refused():
+    """A launch counts its work items in 32 bits: 2^24 - 1 workgroups of 256."""
+    c = cache(H_kv=2)
+    for fn in (L.gdntree_cache_write, L.gdntree_cache_read):
+        assert fn(c, 0, FAKE, 4, FAKE, None, 1 << 20, 1 << 7, 1, FAKE, FAKE, None) == 2
+    assert L.gdntree_cache_commit(cache(L=16), FAKE, 4, FAKE, 1 << 20, 24, 8, FAKE, FAKE, None) == 2
+    assert L.gdntree_attend(cache(), 0, FAKE, 4, FAKE, None, None, 1 << 22, 1, 8, 1, FAKE, 0.1, FAKE, None, 0, None) == 2
+    tree = g.CTree(FAKE, None, None, FAKE, None, None, FAKE)
+    assert L.gdntree_accept_sample(tree, 1 << 20, 24, 8, 100, 1, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 1 << 40, None) == 2
+
+
 def test_no_device_is_reported():
     if torch.cuda.is_available():
         pytest.skip("there is a device")
