@@ -275,3 +275,24 @@ def test_binding_refusals():
         with pytest.raises((ValueError, g.GdnTreeError)):
             g.gdntree_attend(a["q"], kv, a["layer"], a["table"], a["ctx"], tree=a["tree"], n_rows=a["n_rows"],
                              scale=a["scale"], o=a["o"], workspace=a["workspace"])
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with scratch memory of its own, beside each other."""
+    import gdn_draft_tree_amd as g
+    ctx = [5001, 1203]
+    one = setup(g, 2, 33, 4, 2, 128, 64, "bf16", "bf16", ctx, [33, 33], "tree", 3)
+    two = setup(g, 2, 1, 4, 2, 128, 64, "e4m3", "bf16", ctx, [1, 1], "chain", 4)
+    alone = [call(g, x[0], x[1], x[3], ctx, [r, r], x[4]) for x, r in ((one, 33), (two, 1))]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = []
+        for s in streams:
+            s.wait_stream(torch.cuda.current_stream())
+        for s, x, r in zip(streams, (one, two), (33, 1)):
+            with torch.cuda.stream(s):
+                got.append(call(g, x[0], x[1], x[3], ctx, [r, r], x[4]))
+        torch.cuda.synchronize()
+        for a, b in zip(alone, got):
+            assert torch.equal(a, b)

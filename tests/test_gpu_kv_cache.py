@@ -210,3 +210,31 @@ def test_offsets_past_32_bits():
     g.gdntree_cache_commit(kv, table, starts, i32([3, 3]), node, 64)
     a, _ = g.gdntree_cache_read(kv, 1, table, starts, 3)
     assert torch.equal(a[0], k[0, [0, 5, 60]]) and torch.equal(a[1], k[1, :3])
+
+
+def test_other_streams_and_prepared_calls():
+    """The same write, read and commit on the current stream, on another one, and prepared."""
+    import gdn_draft_tree_amd as g
+    gen = torch.Generator().manual_seed(21)
+    table = tables(3, 4, 12, gen)
+    k, v = (make_rows(3, 20, 2, 64, "f32", gen) for _ in range(2))
+    ctx, acc_len, acc_node = i32([30, 0, 7]), i32([3, 1, 4]), i32([[0, 2, 9, -1], [0, -1, -1, -1], [0, 1, 4, 19]])
+    blank = new_cache(g, 2, 12, 2, 16, 64, "e4m3", gen)
+    results = []
+    for how in ("current", "stream", "prepared"):
+        kv = g.KVCache(*(x.clone() for x in (blank.k, blank.v, blank.k_scale, blank.v_scale)))
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        kw = dict(stream=side) if how == "stream" else dict(prepare=True) if how == "prepared" else {}
+        calls = [g.gdntree_cache_write(kv, 1, table, ctx, k, v, **kw),
+                 g.gdntree_cache_commit(kv, table, ctx, acc_len, acc_node, 19, **kw),
+                 g.gdntree_cache_read(kv, 1, table, i32([0, 0, 0]), 50, out_dtype=torch.float32, **kw)]
+        if how == "prepared":
+            for c in calls[:2]:
+                assert c() is None
+            calls[2] = calls[2]()
+        torch.cuda.current_stream().wait_stream(side)
+        results.append([x.cpu() for x in calls[2]] + [torch.from_numpy(x) for x in fields(kv)])
+    for other in results[1:]:
+        for a, b in zip(results[0], other):
+            np.testing.assert_array_equal(a.numpy(), b.numpy())
