@@ -358,6 +358,7 @@ __global__ __launch_bounds__(256) void sample_walk_kernel(SampleParams p, Worksp
     float top = kNegInf;
     bool ok = true;
     unsigned best = 0xffffffffu;
+#pragma unroll 4
     for (int i = 0; i < nc; ++i) {
       ok = ok && st[i].m == st[i].m;
       if (st[i].m > top) { top = st[i].m; best = st[i].s; }  // chunks come in order
@@ -365,8 +366,11 @@ __global__ __launch_bounds__(256) void sample_walk_kernel(SampleParams p, Worksp
     ok = ok && top > kNegInf && top < __builtin_inff();
     double z = 0.0;
     if (!greedy)
-      for (int i = 0; i < nc; ++i)
-        if (st[i].m > kNegInf) z += (double)__uint_as_float(st[i].s) * (double)__builtin_amdgcn_exp2f(rebase(st[i].m, top, c));
+#pragma unroll 4
+      for (int i = 0; i < nc; ++i) {
+        const double x = (double)__uint_as_float(st[i].s) * (double)__builtin_amdgcn_exp2f(rebase(st[i].m, top, c));
+        z += st[i].m > kNegInf ? x : 0.0;
+      }
     s_top[tid] = ok ? top : __builtin_nanf("");
     s_at[tid] = uni * z;
     s_best[tid] = (int)best;
